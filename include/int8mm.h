@@ -358,6 +358,104 @@ int8mm_status int8mm_forward_decode_noalloc(const uint16_t* X, int M, const int8
  * int8mm_get_device_status does for a workspace). */
 int8mm_status int8mm_noalloc_device_status(void* stream, int32_t* n_outliers);
 
+/* ------------------------------------------------------------------------ */
+/* Block-scaled 8-bit floating point (e4m3): product and mixture of experts   */
+/* ------------------------------------------------------------------------ */
+
+/* The paper's 8-bit type is int8; these calls do the same layers with e4m3
+ * codes and one fp32 scale per block of 128, the granularity of the block-wise
+ * codec, in the form in which block-scaled checkpoints are stored.
+ *   Codes of a block of values with absolute maximum a (steps in fp32):
+ *     s = max(RN(a / 448), 2^-126),  code = e4m3(RN(x * RN(1 / s)))  (half to
+ *     even, at most 448 in magnitude),  value = code * s.
+ *   Activations: blocks of 128 consecutive k of one row (the last one may be
+ *   shorter).  Weights: blocks of 128 output channels x 128 k.
+ * There is no outlier decomposition: an outlier costs its own block of 128
+ * some precision and no other.  A row of X with a NaN or an infinity gives NaN
+ * in its own outputs only.
+ * 16-bit tensors are fp16 or bf16 (dtype: INT8MM_F16, INT8MM_BF16); Y has X's
+ * type.  Shape and alignment rules as above, except that codes and scales in
+ * buffers of the caller's own need 16- and 4-byte alignment only.  The
+ * kernels use programmatic dependent launch and read nothing, weights
+ * included, before the earlier work on the stream has finished. */
+enum { INT8MM_F16 = 0, INT8MM_BF16 = 1 };
+
+/* codes (device, M x K e4m3) and scales (device, M x ceil(K/128) fp32) of X
+ * (device, M x K, 16 bits).  Allocates nothing and needs no workspace. */
+int8mm_status int8mm_quantize_fp8(const uint16_t* X, int dtype, int M, int K, uint8_t* codes, float* scales,
+                                  void* stream);
+
+/* A block-scaled weight.  The pointers may come from
+ * int8mm_prepare_weight_fp8 or be the caller's own (a checkpoint's). */
+typedef struct {
+    int32_t K, N;
+    uint8_t* codes;      /* device, N x K e4m3: row n = output channel n, K contiguous */
+    float* scales;       /* device, ceil(N/128) x ceil(K/128) */
+} int8mm_fp8_weight;
+
+/* Bytes of the device buffer int8mm_prepare_weight_fp8 needs (0 when a shape
+ * rule is broken). */
+size_t int8mm_fp8_weight_bytes(int K, int N);
+
+/* Convert W (device, K x N, 16 bits) once.  Stream-ordered; W must stay valid
+ * until the work on `stream` is done. */
+int8mm_status int8mm_prepare_weight_fp8(const uint16_t* W, int dtype, int K, int N, void* buf, size_t buf_bytes,
+                                        int8mm_fp8_weight* out, void* stream);
+
+/* Bytes of device workspace of a product of this shape.  Zero-initialised
+ * like the other workspaces (int8mm_workspace_init), with the same rules of
+ * use; its status is read with int8mm_get_device_status. */
+size_t int8mm_fp8_workspace_bytes(int M, int K, int N);
+
+/* Y (device, M x N) = X W, any M >= 1:
+ *   Y[m,n] = 16-bit( sum_b xs[m,b] * ws[n/128,b] * sum_{k in block b} xq[m,k] wq[n,k] ),
+ * with X's codes and scales formed by the call; the sums of a block are the
+ * tensor cores' fp32 sums, the sum over blocks is fp32.  The result does not
+ * depend on what else runs.
+ * opts may be NULL.  path: INT8MM_PATH_AUTO, _GEMM (tiled, SM pairs) or
+ * _DECODE (weight-streaming, M <= 1024); acc_out must be NULL; events, wait
+ * limit and test flags as for int8mm_forward_ex. */
+int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8mm_fp8_weight* w, uint16_t* Y, void* ws,
+                                 size_t ws_bytes, const int8mm_forward_opts* opts, void* stream);
+
+/* A mixture-of-experts feed-forward layer: E experts of
+ *   y = (silu(x Wg) * (x Wu)) Wd,
+ * Wg and Wu H -> I, Wd I -> H, each stored as in int8mm_fp8_weight, expert
+ * after expert, and a router with one 16-bit row of H per expert (X's dtype).
+ * All pointers are the caller's device memory. */
+typedef struct {
+    int32_t E, H, I;
+    const uint16_t* router;    /* E x H */
+    const uint8_t* gate_codes; /* E x I x H */
+    const float* gate_scales;  /* E x ceil(I/128) x ceil(H/128) */
+    const uint8_t* up_codes;   /* E x I x H */
+    const float* up_scales;
+    const uint8_t* down_codes; /* E x H x I */
+    const float* down_scales;  /* E x ceil(H/128) x ceil(I/128) */
+} int8mm_moe_weight;
+
+/* Bytes of device workspace of a layer call (0 when a rule is broken:
+ * 1 <= T <= 64; H, I >= 16 and multiples of 16, at most 131072;
+ * 1 <= E <= 256; 1 <= top_k <= min(E, 16)).  Zero-initialised. */
+size_t int8mm_moe_workspace_bytes(int T, int H, int I, int E, int top_k);
+
+/* Y (device, T x H) = the layer applied to T tokens X (device, T x H), for
+ * the few tokens of a decode step (T <= 64), in three kernels:
+ *   scores l = X R^T (64-bit sums), p = softmax(l) over the experts; each token
+ *   takes its top_k experts (ties to the lower index; a NaN score counts as
+ *   lower than any number) with weight p, or p / (sum of its chosen p) if
+ *   renormalize is not 0;
+ *   h = silu(g) * u with g and u the block-scaled products of X (fp32, not
+ *   rounded to 16 bits), h quantised by the rule above in blocks of 128;
+ *   Y = 16-bit( sum over the token's experts of weight * (h Wd) ), fp32 sums.
+ * topk_ids (device, T x top_k int32, best first) and topk_weights (device,
+ * T x top_k fp32) receive the routing; each may be NULL.  Only the weights of
+ * chosen experts are read.  opts may be NULL; path and events must be unset.
+ */
+int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const int8mm_moe_weight* w, int top_k,
+                                     int renormalize, uint16_t* Y, int32_t* topk_ids, float* topk_weights, void* ws,
+                                     size_t ws_bytes, const int8mm_forward_opts* opts, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

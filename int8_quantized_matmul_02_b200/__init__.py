@@ -15,6 +15,7 @@ attention-projection layers of a transformer.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -28,6 +29,8 @@ __all__ = [
     "block_quantize", "block_dequantize",
     "Int4Weight", "prepare_weight_int4", "forward_int4", "unpack_int4_codes",
     "GroupedWeight", "prepare_weight_grouped", "forward_grouped",
+    "Fp8Weight", "Fp8Workspace", "quantize_fp8", "prepare_weight_fp8", "weight_fp8", "forward_fp8",
+    "MoeFp8Weight", "MoeWorkspace", "prepare_moe_weight_fp8", "moe_weight_fp8", "forward_moe_fp8",
     "Int8mmError", "PATH_AUTO", "PATH_GEMM", "PATH_DECODE",
 ]
 
@@ -385,3 +388,249 @@ def forward_grouped(X: torch.Tensor, w: GroupedWeight, threshold: float = 6.0, *
                                               ctypes.c_void_p(workspace.buf.data_ptr()), workspace.nbytes,
                                               ctypes.byref(opts), _stream(stream)), "int8mm_forward_grouped")
     return Y
+
+
+# ---------------------------------------------------------------------------- block-scaled e4m3
+
+_DTYPES = {torch.float16: _abi.F16, torch.bfloat16: _abi.BF16}
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(device: torch.device, stream=None):
+    """A context with `device` current, and `stream` if given, so that what a
+    call allocates belongs to the stream that it launches on."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _same_device(what: str, device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{what} must be on one device")
+
+
+def _check_out(t: torch.Tensor | None, name: str, shape, dtype: torch.dtype, device: torch.device) -> None:
+    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def quantize_fp8(X: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Block-scaled e4m3 codes of a float16 or bfloat16 CUDA matrix: one scale
+    per row and 128 consecutive columns (the last block may be shorter).
+    Returns (codes float8_e4m3fn M x K, scales float32 M x ceil(K/128)); a
+    value is code * scale."""
+    if not (X.is_cuda and X.dtype in _DTYPES and X.dim() == 2 and X.is_contiguous()):
+        raise ValueError("X must be a contiguous 2-D float16 or bfloat16 CUDA tensor")
+    M, K = X.shape
+    kb = (K + 127) // 128
+    _check_out(codes, "codes", (M, K), torch.float8_e4m3fn, X.device)
+    _check_out(scales, "scales", (M, kb), torch.float32, X.device)
+    with _on(X.device, stream):
+        codes = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=X.device) if codes is None else codes
+        scales = torch.empty(M, kb, dtype=torch.float32, device=X.device) if scales is None else scales
+        _abi.check(_abi.load().int8mm_quantize_fp8(X.data_ptr(), _DTYPES[X.dtype], M, K, codes.data_ptr(),
+                                                   scales.data_ptr(), _stream(stream)), "int8mm_quantize_fp8")
+    return codes, scales
+
+
+class Fp8Weight:
+    """A block-scaled e4m3 weight (see ``int8mm_fp8_weight`` in the header)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.codes = codes      # N x K float8_e4m3fn
+        self.scales = scales    # ceil(N/128) x ceil(K/128) float32
+        self.N, self.K = codes.shape
+        self.struct = _abi.Fp8Weight(self.K, self.N, codes.data_ptr(), scales.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+
+def _check_codes(what: str, codes: torch.Tensor, scales: torch.Tensor, lead=()) -> None:
+    n = len(lead)
+    if not (codes.is_cuda and codes.dtype == torch.float8_e4m3fn and codes.dim() == n + 2 and codes.is_contiguous()
+            and codes.shape[:n] == torch.Size(lead)):
+        raise ValueError(f"{what} codes must be a contiguous float8_e4m3fn CUDA tensor of shape {(*lead, 'N', 'K')}")
+    N, K = codes.shape[n:]
+    if N < 16 or K < 16 or N % 16 or K % 16:
+        raise ValueError(f"{what}: N and K must be multiples of 16, found N={N}, K={K}")
+    shape = (*lead, (N + 127) // 128, (K + 127) // 128)
+    if scales.dtype != torch.float32 or scales.shape != shape or not scales.is_contiguous():
+        raise ValueError(f"{what} scales must be a contiguous float32 tensor of shape {shape}")
+    _same_device(f"{what} codes and scales", codes.device, scales)
+
+
+def weight_fp8(codes: torch.Tensor, scales: torch.Tensor) -> Fp8Weight:
+    """The weight whose codes (float8_e4m3fn N x K, one row per output channel)
+    and 128 x 128 block scales (float32 ceil(N/128) x ceil(K/128)) the caller
+    has, from a block-scaled checkpoint for instance.  Nothing is copied."""
+    _check_codes("weight", codes, scales)
+    return Fp8Weight(codes, scales)
+
+
+def prepare_weight_fp8(W: torch.Tensor, stream=None) -> Fp8Weight:
+    """Convert a K x N float16 or bfloat16 CUDA weight to e4m3 codes with one
+    scale per 128 x 128 block (once, at load)."""
+    lib = _abi.load()
+    if not (W.is_cuda and W.dtype in _DTYPES and W.dim() == 2 and W.is_contiguous()):
+        raise ValueError("W must be a contiguous 2-D float16 or bfloat16 CUDA tensor (K x N)")
+    K, N = W.shape
+    nbytes = lib.int8mm_fp8_weight_bytes(K, N)
+    if nbytes == 0:
+        raise Int8mmError(1, f"int8mm_fp8_weight_bytes(K={K}, N={N})")
+    st = _abi.Fp8Weight()
+    with _on(W.device, stream):
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+        _abi.check(lib.int8mm_prepare_weight_fp8(W.data_ptr(), _DTYPES[W.dtype], K, N, buf.data_ptr(), nbytes,
+                                                 ctypes.byref(st), _stream(stream)), "int8mm_prepare_weight_fp8")
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    return Fp8Weight(_view(buf, st.codes, N * K, torch.float8_e4m3fn, (N, K)),
+                     _view(buf, st.scales, nb * kb, torch.float32, (nb, kb)))
+
+
+class Fp8Workspace:
+    """Device scratch of one block-scaled product's shape; zero-filled at
+    creation.  Two products that may overlap on the GPU need two of them."""
+
+    def __init__(self, M: int, K: int, N: int, device=None):
+        self.M, self.K, self.N = M, K, N
+        self.nbytes = _abi.load().int8mm_fp8_workspace_bytes(M, K, N)
+        if self.nbytes == 0:
+            raise Int8mmError(1, f"int8mm_fp8_workspace_bytes(M={M}, K={K}, N={N})")
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+    reset = Workspace.reset
+
+
+def _fp8_opts(path: str, wait_limit_ns: int, test_flags: int):
+    if path == "auto" and not wait_limit_ns and not test_flags:
+        return None
+    return ctypes.byref(_abi.ForwardOpts(_PATHS[path], None, int(wait_limit_ns), None, None, int(test_flags)))
+
+
+def forward_fp8(X: torch.Tensor, w: Fp8Weight, *, out: torch.Tensor | None = None,
+                workspace: Fp8Workspace | None = None, path: str = "auto", wait_limit_ns: int = 0, test_flags: int = 0,
+                stream=None) -> torch.Tensor:
+    """Y = X W with X (M x K float16 or bfloat16, on the weight's device)
+    quantised to e4m3 per row and block of 128 by the call, and the
+    block-scaled weight; fp32 sums, Y in X's type.  path: "auto", "gemm"
+    (tiled) or "decode" (weight-streaming, M <= 1024)."""
+    dev = w.codes.device
+    if X.dtype not in _DTYPES or X.dim() != 2 or X.shape[1] != w.K or X.device != dev or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous float16 or bfloat16 tensor of shape (M, {w.K}) on {dev}")
+    M = X.shape[0]
+    if workspace is not None and ((workspace.M, workspace.K, workspace.N) != (M, w.K, w.N)
+                                  or workspace.buf.device != dev):
+        raise ValueError("workspace was made for another shape or device")
+    _check_out(out, "out", (M, w.N), X.dtype, dev)
+    with _on(dev, stream):
+        if workspace is None:
+            workspace = Fp8Workspace(M, w.K, w.N, device=dev)
+        Y = out if out is not None else torch.empty(M, w.N, dtype=X.dtype, device=dev)
+        _abi.check(_abi.load().int8mm_forward_fp8(X.data_ptr(), _DTYPES[X.dtype], M, w.ref, Y.data_ptr(),
+                                                  workspace.buf.data_ptr(), workspace.nbytes,
+                                                  _fp8_opts(path, wait_limit_ns, test_flags), _stream(stream)),
+                   "int8mm_forward_fp8")
+    return Y
+
+
+# ---------------------------------------------------------------------------- mixture of experts
+
+class MoeFp8Weight:
+    """The weights of a mixture-of-experts feed-forward layer (see
+    ``int8mm_moe_weight`` in the header)."""
+
+    def __init__(self, router: torch.Tensor, gate, up, down):
+        self.router, self.gate, self.up, self.down = router, gate, up, down
+        self.E, self.I, self.H = gate[0].shape
+        self.struct = _abi.MoeWeight(self.E, self.H, self.I, router.data_ptr(),
+                                     *(t.data_ptr() for pair in (gate, up, down) for t in pair))
+        self.ref = ctypes.byref(self.struct)
+
+
+def moe_weight_fp8(router: torch.Tensor, gate, up, down) -> MoeFp8Weight:
+    """The layer of E experts y = (silu(x Wg) * (x Wu)) Wd from weights that
+    are block-scaled e4m3 already.  router: E x H float16 or bfloat16 (the type
+    of the layer's X); gate, up: (codes float8_e4m3fn E x I x H, scales float32
+    E x ceil(I/128) x ceil(H/128)); down: (codes E x H x I, scales).  Nothing
+    is copied."""
+    if not (router.is_cuda and router.dtype in _DTYPES and router.dim() == 2 and router.is_contiguous()):
+        raise ValueError("router must be a contiguous 2-D float16 or bfloat16 CUDA tensor (E x H)")
+    E, H = router.shape
+    gate, up, down = tuple(gate), tuple(up), tuple(down)
+    for what, (codes, scales) in (("gate", gate), ("up", up), ("down", down)):
+        _check_codes(what, codes, scales, (E,))
+    inner = gate[0].shape[1]
+    if gate[0].shape != (E, inner, H) or up[0].shape != (E, inner, H) or down[0].shape != (E, H, inner):
+        raise ValueError("gate and up must be E x I x H and down E x H x I, with the router's E and H")
+    _same_device("the layer's weights", router.device, gate[0], up[0], down[0])
+    return MoeFp8Weight(router, gate, up, down)
+
+
+def prepare_moe_weight_fp8(router: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
+                           stream=None) -> MoeFp8Weight:
+    """Convert a layer's 16-bit weights once (at load): router E x H; gate and
+    up E x H x I, down E x I x H (each expert K x N, as prepare_weight_fp8
+    takes it), float16 or bfloat16 CUDA tensors."""
+    for what, W in (("gate", gate), ("up", up), ("down", down)):
+        if not (W.is_cuda and W.dtype in _DTYPES and W.dim() == 3 and W.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous 3-D float16 or bfloat16 CUDA tensor")
+
+    def convert(W):
+        parts = [prepare_weight_fp8(We, stream) for We in W]
+        with _on(W.device, stream):
+            return torch.stack([q.codes for q in parts]), torch.stack([q.scales for q in parts])
+
+    return moe_weight_fp8(router, convert(gate), convert(up), convert(down))
+
+
+class MoeWorkspace:
+    """Device scratch of a mixture-of-experts layer for T tokens; zero-filled
+    at creation.  Two calls that may overlap on the GPU need two of them."""
+
+    def __init__(self, T: int, w: MoeFp8Weight, top_k: int, device=None):
+        self.T, self.H, self.I, self.E, self.top_k = T, w.H, w.I, w.E, top_k
+        self.nbytes = _abi.load().int8mm_moe_workspace_bytes(T, w.H, w.I, w.E, top_k)
+        if self.nbytes == 0:
+            raise Int8mmError(1, f"int8mm_moe_workspace_bytes(T={T}, H={w.H}, I={w.I}, E={w.E}, top_k={top_k})")
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or w.router.device)
+
+    reset = Workspace.reset
+
+
+def forward_moe_fp8(X: torch.Tensor, w: MoeFp8Weight, top_k: int, *, renormalize: bool = True,
+                    out: torch.Tensor | None = None, workspace: MoeWorkspace | None = None,
+                    return_routing: bool = False, wait_limit_ns: int = 0, test_flags: int = 0, stream=None):
+    """The mixture-of-experts layer on a few tokens: X is T x H (T <= 64) in the
+    router's type and on its device.  Each token takes the top_k experts of
+    softmax(X router^T), ties to the lower index, with those probabilities as
+    weights (renormalize: divided by their sum).  Returns Y, T x H in X's type,
+    and with return_routing also the experts (int32 T x top_k, best first) and
+    their weights (float32 T x top_k)."""
+    dev = w.router.device
+    if X.dtype != w.router.dtype or X.dim() != 2 or X.shape[1] != w.H or X.device != dev or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous {w.router.dtype} tensor of shape (T, {w.H}) on {dev}")
+    T = X.shape[0]
+    if workspace is not None and (
+            (workspace.T, workspace.H, workspace.I, workspace.E, workspace.top_k) != (T, w.H, w.I, w.E, top_k)
+            or workspace.buf.device != dev):
+        raise ValueError("workspace was made for another shape or device")
+    _check_out(out, "out", (T, w.H), X.dtype, dev)
+    ids = wts = None
+    with _on(dev, stream):
+        if workspace is None:
+            workspace = MoeWorkspace(T, w, top_k)
+        Y = out if out is not None else torch.empty(T, w.H, dtype=X.dtype, device=dev)
+        if return_routing:
+            ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
+            wts = torch.empty(T, top_k, dtype=torch.float32, device=dev)
+        _abi.check(_abi.load().int8mm_forward_moe_fp8(
+            X.data_ptr(), _DTYPES[X.dtype], T, w.ref, top_k, int(bool(renormalize)), Y.data_ptr(),
+            ids.data_ptr() if return_routing else None, wts.data_ptr() if return_routing else None,
+            workspace.buf.data_ptr(), workspace.nbytes, _fp8_opts("auto", wait_limit_ns, test_flags),
+            _stream(stream)), "int8mm_forward_moe_fp8")
+    return (Y, ids, wts) if return_routing else Y

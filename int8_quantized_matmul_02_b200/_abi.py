@@ -23,6 +23,7 @@ STATUS_NAMES = {
     7: "INT8MM_ERR_OUTLIER_OVERFLOW",
 }
 PATH_AUTO, PATH_GEMM, PATH_DECODE, PATH_GEMM_1SM = 0, 1, 2, 3
+F16, BF16 = 0, 1
 
 # Every symbol the header declares.
 EXPORTS = (
@@ -35,6 +36,8 @@ EXPORTS = (
     "int8mm_int4_weight_bytes", "int8mm_prepare_weight_int4", "int8mm_forward_int4",
     "int8mm_grouped_weight_bytes", "int8mm_prepare_weight_grouped", "int8mm_grouped_workspace_bytes",
     "int8mm_grouped_workspace_view_get", "int8mm_forward_grouped",
+    "int8mm_quantize_fp8", "int8mm_fp8_weight_bytes", "int8mm_prepare_weight_fp8", "int8mm_fp8_workspace_bytes",
+    "int8mm_forward_fp8", "int8mm_moe_workspace_bytes", "int8mm_forward_moe_fp8",
 )
 
 
@@ -63,6 +66,17 @@ class GroupedWeight(ctypes.Structure):
 class Int4Weight(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("G", ctypes.c_int32),
                 ("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
+
+
+class Fp8Weight(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class MoeWeight(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("router", ctypes.c_void_p),
+                ("gate_codes", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
+                ("up_codes", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+                ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
 
 
 class ForwardOpts(ctypes.Structure):
@@ -143,6 +157,21 @@ def load(path: str | None = None):
     lib.int8mm_forward_grouped.argtypes = [P, I, ctypes.POINTER(GroupedWeight), F, I, P, P, S,
                                            ctypes.POINTER(ForwardOpts), P]
     lib.int8mm_forward_grouped.restype = I
+    lib.int8mm_quantize_fp8.argtypes = [P, I, I, I, P, P, P]
+    lib.int8mm_quantize_fp8.restype = I
+    lib.int8mm_fp8_weight_bytes.argtypes = [I, I]
+    lib.int8mm_fp8_weight_bytes.restype = S
+    lib.int8mm_prepare_weight_fp8.argtypes = [P, I, I, I, P, S, ctypes.POINTER(Fp8Weight), P]
+    lib.int8mm_prepare_weight_fp8.restype = I
+    lib.int8mm_fp8_workspace_bytes.argtypes = [I, I, I]
+    lib.int8mm_fp8_workspace_bytes.restype = S
+    lib.int8mm_forward_fp8.argtypes = [P, I, I, ctypes.POINTER(Fp8Weight), P, P, S, ctypes.POINTER(ForwardOpts), P]
+    lib.int8mm_forward_fp8.restype = I
+    lib.int8mm_moe_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.int8mm_moe_workspace_bytes.restype = S
+    lib.int8mm_forward_moe_fp8.argtypes = [P, I, I, ctypes.POINTER(MoeWeight), I, I, P, P, P, P, S,
+                                           ctypes.POINTER(ForwardOpts), P]
+    lib.int8mm_forward_moe_fp8.restype = I
     if path is None:
         _lib = lib
     return lib

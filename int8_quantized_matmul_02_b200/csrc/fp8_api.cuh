@@ -1,0 +1,429 @@
+// C-ABI of the block-scaled e4m3 operators (included by int8mm_api.cu, whose
+// helpers it uses): argument checks, layouts, tensor maps and launches.
+
+namespace {
+
+constexpr int kFp8RowsMaxM = 1024;  // rows the weight-streaming kernel takes (its workspace is sized for them)
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxTopK = 16;
+
+bool dtype_ok(int dtype) { return dtype == INT8MM_F16 || dtype == INT8MM_BF16; }
+
+// Columns of B of the weight-streaming kernel for M rows.
+int fp8_rows_nt(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+struct Fp8Layout {
+    size_t codes, scales, total;
+};
+
+Fp8Layout fp8_weight_layout(int K, int N) {
+    Fp8Layout L{};
+    size_t o = align_up((size_t)N * K, 256);
+    L.scales = o;
+    L.total = align_up(o + (size_t)cdiv(N, 128) * cdiv(K, 128) * 4, 256);
+    return L;
+}
+
+struct Fp8WsLayout {
+    size_t status, codes, scales, tickets, parts, total;
+};
+
+Fp8WsLayout fp8_ws_layout(int M, int K, int N) {
+    Fp8WsLayout L{};
+    size_t o = 256;
+    L.codes = o;
+    o = align_up(o + (size_t)M * K, 256);
+    L.scales = o;
+    o = align_up(o + (size_t)M * cdiv(K, 128) * 4, 256);
+    L.tickets = o;
+    L.parts = o;
+    if (M <= kFp8RowsMaxM) {
+        const int nt = fp8_rows_nt(M);
+        o = align_up(o + (size_t)cdiv(N, 128) * cdiv(M, nt) * 4, 256);
+        L.parts = o;
+        o = align_up(o + (size_t)2 * kFRMaxCtas * nt * 128 * 4, 256);
+    }
+    L.total = o;
+    return L;
+}
+
+struct MoeWsLayout {
+    size_t status, logits, ids, wts, active, tickets, xq, xs, hq, hs, parts, total;
+    size_t t_gate, t_down;  // tickets of the two products, after the router's
+};
+
+// Chosen experts of T tokens: at most min(E, T * top_k).
+int moe_max_active(int T, int E, int top_k) { return (int)std::min<long long>(E, (long long)T * top_k); }
+
+MoeWsLayout moe_ws_layout(int T, int H, int I, int E, int top_k) {
+    MoeWsLayout L{};
+    const int A = moe_max_active(T, E, top_k);
+    size_t o = 256;
+    const auto take = [&o](size_t bytes) {
+        const size_t at = o;
+        o = align_up(o + bytes, 256);
+        return at;
+    };
+    L.logits = take((size_t)T * E * 8);
+    L.ids = take((size_t)T * top_k * 4);
+    L.wts = take((size_t)T * top_k * 4);
+    L.active = take((size_t)(A + 1) * 4);
+    L.tickets = take((size_t)(T + 1) * 4);
+    L.t_gate = take((size_t)A * cdiv(I, 128) * 4);
+    L.t_down = take((size_t)cdiv(H, 128) * 4);
+    L.xq = take((size_t)T * H);
+    L.xs = take((size_t)T * cdiv(H, 128) * 4);
+    L.hq = take((size_t)A * T * I);
+    L.hs = take((size_t)A * T * cdiv(I, 128) * 4);
+    L.parts = take((size_t)2 * kFRMaxCtas * 2 * fp8_rows_nt(T) * 128 * 4);
+    L.total = o;
+    return L;
+}
+
+bool moe_shape_ok(int T, int H, int I, int E, int top_k) {
+    return T >= 1 && T <= kMoeMaxTokens && shape_ok(T, H, I) && I <= kMaxK && E >= 1 && E <= kMaxExperts &&
+           top_k >= 1 && top_k <= kMoeMaxTopK && top_k <= E;
+}
+
+// 3-D tensor of `depth` row-major matrices of `outer` rows x `inner` bytes,
+// with a 128-byte swizzled box of 128 x box_outer x 1.
+bool make_map3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t depth, uint32_t box_outer) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {inner, outer, depth};
+    cuuint64_t strides[2] = {inner, inner * outer};
+    cuuint32_t box[3] = {128, box_outer, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Opt in to a kernel's shared memory once per device.
+template <auto Kern>
+cudaError_t fp8_opt_in(int dev, int smem) {
+    static std::atomic<uint64_t> done{0};  // one bit per device (current_device admits fewer than 64)
+    if ((done.load(std::memory_order_acquire) >> dev) & 1u) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
+cudaError_t launch_quant_fp8(const uint16_t* X, int dtype, int M, int K, uint8_t* codes, float* scales, long long sm,
+                             long long sb, int sms, cudaStream_t s) {
+    const int KB = cdiv(K, 128);
+    const long long nblocks = (long long)M * KB;
+    const long long per = (long long)(kQuantThreads / 16) * kQuantBlocks;
+    const int grid = (int)std::max<long long>(1, std::min<long long>((nblocks + per - 1) / per, (long long)sms * 16));
+    return dtype == INT8MM_F16
+               ? launch(k_quant_fp8<F16>, dim3(grid), dim3(kQuantThreads), 0, s, true, X, nblocks, K, KB, codes, scales,
+                        sm, sb)
+               : launch(k_quant_fp8<BF16>, dim3(grid), dim3(kQuantThreads), 0, s, true, X, nblocks, K, KB, codes,
+                        scales, sm, sb);
+}
+
+template <int kMode, int kNT, bool kFuse, typename T>
+cudaError_t launch_rows(int dev, int grid, const CUtensorMap& tw, const CUtensorMap& tw2, const CUtensorMap& tx,
+                        const Fp8RowsParams& p, cudaStream_t s, bool pdl) {
+    constexpr int smem = fr_smem_bytes<kMode, kNT>();
+    static_assert(smem <= kMaxSmemOptin, "shared memory of one SM");
+    cudaError_t e = fp8_opt_in<k_fp8_rows<kMode, kNT, kFuse, T>>(dev, smem);
+    if (e != cudaSuccess) return e;
+    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(kFRThreads), smem, s, pdl, tw, tw2, tx, p);
+}
+
+template <int kBN, typename T>
+cudaError_t launch_gemm_fp8(int dev, int grid, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
+                            const Fp8GemmParams& p, cudaStream_t s, bool pdl) {
+    cudaError_t e = fp8_opt_in<k_gemm_fp8_2sm<kBN, T>>(dev, f8_smem_bytes(kBN));
+    if (e != cudaSuccess) return e;
+    return launch_ex(k_gemm_fp8_2sm<kBN, T>, dim3(grid), dim3(kF8Threads), f8_smem_bytes(kBN), s, pdl, 2, ta, tb, ty, p);
+}
+
+struct Fp8Opts {
+    int path;
+    cudaEvent_t ev0, ev1;
+    uint64_t wait_ns;
+    uint32_t test_flags;
+};
+
+bool fp8_opts(const int8mm_forward_opts* o, Fp8Opts* out) {
+    *out = Fp8Opts{INT8MM_PATH_AUTO, nullptr, nullptr, kDefaultWaitNs, 0};
+    if (!o) return true;
+    if (o->acc_out) return false;  // there are no int32 sums
+    out->path = o->path;
+    out->ev0 = reinterpret_cast<cudaEvent_t>(o->main_start_event);
+    out->ev1 = reinterpret_cast<cudaEvent_t>(o->main_stop_event);
+    if (o->wait_limit_ns) out->wait_ns = o->wait_limit_ns;
+    out->test_flags = o->test_flags;
+    return (out->ev0 == nullptr) == (out->ev1 == nullptr);
+}
+
+// Whether the weight-streaming kernel takes a product of M rows.
+bool fp8_rows_path(int M, int N, int sms) {
+    (void)N;
+    (void)sms;
+    return M <= 128;
+}
+
+}  // namespace
+
+extern "C" {
+
+int8mm_status int8mm_quantize_fp8(const uint16_t* X, int dtype, int M, int K, uint8_t* codes, float* scales,
+                                  void* stream) {
+    if (!X || !codes || !scales || !dtype_ok(dtype) || !shape_ok(M, K, 16)) return INT8MM_ERR_INVALID_ARGUMENT;
+    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return INT8MM_ERR_MISALIGNED;
+    int dev;
+    DeviceInfo* info;
+    int8mm_status st = current_device(&dev, &info);
+    if (st != INT8MM_OK) return st;
+    return cuda_status(launch_quant_fp8(X, dtype, M, K, codes, scales, cdiv(K, 128), 1, info->sm_count,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t int8mm_fp8_weight_bytes(int K, int N) {
+    if (!shape_ok(1, K, N)) return 0;
+    return fp8_weight_layout(K, N).total;
+}
+
+int8mm_status int8mm_prepare_weight_fp8(const uint16_t* W, int dtype, int K, int N, void* buf, size_t buf_bytes,
+                                        int8mm_fp8_weight* out, void* stream) {
+    if (!W || !buf || !out || !dtype_ok(dtype) || !shape_ok(1, K, N)) return INT8MM_ERR_INVALID_ARGUMENT;
+    if (!aligned(W, 16) || !aligned(buf, 256)) return INT8MM_ERR_MISALIGNED;
+    const Fp8Layout L = fp8_weight_layout(K, N);
+    if (buf_bytes < L.total) return INT8MM_ERR_WORKSPACE_TOO_SMALL;
+    int dev;
+    DeviceInfo* info;
+    int8mm_status st = current_device(&dev, &info);
+    if (st != INT8MM_OK) return st;
+    uint8_t* b = static_cast<uint8_t*>(buf);
+    int8mm_fp8_weight w{};
+    w.K = K;
+    w.N = N;
+    w.codes = b;
+    w.scales = reinterpret_cast<float*>(b + L.scales);
+    const dim3 grid(cdiv(N, 128), cdiv(K, 128));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == INT8MM_F16
+                              ? launch(k_quant_weight_fp8<F16>, grid, dim3(256), 0, s, false, W, K, N, w.codes, w.scales)
+                              : launch(k_quant_weight_fp8<BF16>, grid, dim3(256), 0, s, false, W, K, N, w.codes, w.scales);
+    if (e != cudaSuccess) return cuda_status(e);
+    *out = w;
+    return INT8MM_OK;
+}
+
+size_t int8mm_fp8_workspace_bytes(int M, int K, int N) {
+    if (!shape_ok(M, K, N)) return 0;
+    return fp8_ws_layout(M, K, N).total;
+}
+
+int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8mm_fp8_weight* w, uint16_t* Y, void* ws,
+                                 size_t ws_bytes, const int8mm_forward_opts* opts, void* stream) {
+    if (!X || !w || !Y || !ws || !w->codes || !w->scales || !dtype_ok(dtype)) return INT8MM_ERR_INVALID_ARGUMENT;
+    const int K = w->K, N = w->N;
+    Fp8Opts o;
+    if (!shape_ok(M, K, N) || !fp8_opts(opts, &o)) return INT8MM_ERR_INVALID_ARGUMENT;
+    if (o.path != INT8MM_PATH_AUTO && o.path != INT8MM_PATH_GEMM && o.path != INT8MM_PATH_DECODE)
+        return INT8MM_ERR_INVALID_ARGUMENT;
+    if (o.path == INT8MM_PATH_DECODE && M > kFp8RowsMaxM) return INT8MM_ERR_INVALID_ARGUMENT;
+    if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(ws, 256) || !aligned(w->codes, 16) || !aligned(w->scales, 4))
+        return INT8MM_ERR_MISALIGNED;
+    const Fp8WsLayout L = fp8_ws_layout(M, K, N);
+    if (ws_bytes < L.total) return INT8MM_ERR_WORKSPACE_TOO_SMALL;
+    int dev;
+    DeviceInfo* info;
+    int8mm_status st = current_device(&dev, &info);
+    if (st != INT8MM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    uint8_t* xq = b + L.codes;
+    float* xs = reinterpret_cast<float*>(b + L.scales);
+    const int KB = cdiv(K, 128), sms = std::min(info->sm_count, kFRMaxCtas);
+    const bool f16 = dtype == INT8MM_F16, timed = o.ev0 != nullptr;
+    const bool rows = o.path == INT8MM_PATH_DECODE || (o.path == INT8MM_PATH_AUTO && fp8_rows_path(M, N, sms));
+    const int nt = fp8_rows_nt(M);
+    const bool fuse = rows && nt <= 32;
+    cudaError_t e = cudaSuccess;
+    if (!fuse) e = launch_quant_fp8(X, dtype, M, K, xq, xs, 1, M, info->sm_count, s);
+    if (e != cudaSuccess) return cuda_status(e);
+    CUtensorMap ta, tb;
+    if (rows) {
+        Fp8RowsParams p{};
+        p.M = M;
+        p.N = N;
+        p.K = K;
+        p.KB = KB;
+        p.NB = cdiv(N, 128);
+        p.MB = cdiv(M, nt);
+        p.X = X;
+        p.xs = xs;
+        p.ws = w->scales;
+        p.Y = Y;
+        p.parts = reinterpret_cast<float*>(b + L.parts);
+        p.tickets = reinterpret_cast<unsigned*>(b + L.tickets);
+        p.status = reinterpret_cast<int*>(b + L.status);
+        p.wait_limit_ns = o.wait_ns;
+        p.test_flags = o.test_flags;
+        if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 128)) return INT8MM_ERR_CUDA;
+        tb = ta;  // unused when the codes are made in the kernel
+        if (!fuse && !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, (uint32_t)nt)) return INT8MM_ERR_CUDA;
+        const long long tiles = (long long)p.NB * p.MB;
+        const int grid = fr_shares(tiles * KB, tiles, sms);
+        if (timed) e = cudaEventRecord(o.ev0, s);
+        if (e != cudaSuccess) return cuda_status(e);
+        const bool pdl = !timed;
+#define I8_ROWS(NT, FUSE)                                                                           \
+    (f16 ? launch_rows<kRows, NT, FUSE, F16>(dev, grid, ta, ta, tb, p, s, pdl)                      \
+         : launch_rows<kRows, NT, FUSE, BF16>(dev, grid, ta, ta, tb, p, s, pdl))
+        e = nt == 16 ? I8_ROWS(16, true) : nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
+#undef I8_ROWS
+    } else {
+        constexpr int bn = 256;
+        CUtensorMap ty;
+        if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, 128) ||
+            !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, bn / 2) ||
+            !make_map(&ty, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
+                      (uint64_t)N * 2, 64, 32))
+            return INT8MM_ERR_CUDA;
+        Fp8GemmParams p{};
+        p.M = M;
+        p.N = N;
+        p.KB = KB;
+        p.num_m_blocks = cdiv(M, kF8BM);
+        p.num_n_blocks = cdiv(N, bn);
+        if ((long long)p.num_m_blocks * p.num_n_blocks > INT32_MAX / 2) return INT8MM_ERR_INVALID_ARGUMENT;
+        p.num_tiles = p.num_m_blocks * p.num_n_blocks;
+        // the largest group of row blocks whose codes fit in 48 MB of L2, at least 8
+        const int fit = (int)std::min<uint64_t>(1u << 20, (48ull << 20) / ((uint64_t)kF8BM * (uint64_t)K));
+        p.group_m = std::min(std::max(8, fit), p.num_m_blocks);
+        p.xs = xs;
+        p.xs_pitch = M;
+        p.ws = w->scales;
+        p.status = reinterpret_cast<int*>(b + L.status);
+        p.wait_limit_ns = o.wait_ns;
+        p.test_flags = o.test_flags;
+        const int grid = 2 * std::min(p.num_tiles, info->sm_count / 2);
+        if (timed) e = cudaEventRecord(o.ev0, s);
+        if (e != cudaSuccess) return cuda_status(e);
+        e = f16 ? launch_gemm_fp8<bn, F16>(dev, grid, ta, tb, ty, p, s, !timed)
+                : launch_gemm_fp8<bn, BF16>(dev, grid, ta, tb, ty, p, s, !timed);
+    }
+    if (e == cudaSuccess && timed) e = cudaEventRecord(o.ev1, s);
+    return cuda_status(e);
+}
+
+size_t int8mm_moe_workspace_bytes(int T, int H, int I, int E, int top_k) {
+    if (!moe_shape_ok(T, H, I, E, top_k)) return 0;
+    return moe_ws_layout(T, H, I, E, top_k).total;
+}
+
+int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const int8mm_moe_weight* w, int top_k,
+                                     int renormalize, uint16_t* Y, int32_t* topk_ids, float* topk_weights, void* ws,
+                                     size_t ws_bytes, const int8mm_forward_opts* opts, void* stream) {
+    if (!X || !w || !Y || !ws || !dtype_ok(dtype) || !w->router || !w->gate_codes || !w->gate_scales || !w->up_codes ||
+        !w->up_scales || !w->down_codes || !w->down_scales)
+        return INT8MM_ERR_INVALID_ARGUMENT;
+    const int H = w->H, I = w->I, E = w->E;
+    Fp8Opts o;
+    if (!moe_shape_ok(T, H, I, E, top_k) || !fp8_opts(opts, &o) || o.path != INT8MM_PATH_AUTO || o.ev0)
+        return INT8MM_ERR_INVALID_ARGUMENT;
+    if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(ws, 256) || !aligned(w->router, 16) ||
+        !aligned(w->gate_codes, 16) || !aligned(w->up_codes, 16) || !aligned(w->down_codes, 16) ||
+        !aligned(w->gate_scales, 4) || !aligned(w->up_scales, 4) || !aligned(w->down_scales, 4) ||
+        !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+        return INT8MM_ERR_MISALIGNED;
+    const MoeWsLayout L = moe_ws_layout(T, H, I, E, top_k);
+    if (ws_bytes < L.total) return INT8MM_ERR_WORKSPACE_TOO_SMALL;
+    int dev;
+    DeviceInfo* info;
+    int8mm_status st = current_device(&dev, &info);
+    if (st != INT8MM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    const int A = moe_max_active(T, E, top_k), HB = cdiv(H, 128), IB = cdiv(I, 128), nt = fp8_rows_nt(T);
+    const int ctas = std::min(info->sm_count, kFRMaxCtas);
+    const bool f16 = dtype == INT8MM_F16;
+    int32_t* ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(b + L.ids);
+    float* wts = topk_weights ? topk_weights : reinterpret_cast<float*>(b + L.wts);
+
+    CUtensorMap tg, tu, td, tx, th;
+    if (!make_map3(&tg, w->gate_codes, H, I, E, 128) || !make_map3(&tu, w->up_codes, H, I, E, 128) ||
+        !make_map3(&td, w->down_codes, I, H, E, 128) ||
+        !make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, b + L.xq, H, T, H, 128, (uint32_t)nt) ||
+        !make_map3(&th, b + L.hq, I, T, A, (uint32_t)nt))
+        return INT8MM_ERR_CUDA;
+
+    RouteParams r{};
+    r.X = X;
+    r.R = w->router;
+    r.T = T;
+    r.H = H;
+    r.E = E;
+    r.top_k = top_k;
+    r.renorm = renormalize != 0;
+    const int tt = T == 1 ? 1 : 4;
+    r.log_blocks = cdiv(E, kRouteExperts) * cdiv(T, tt);
+    r.logits = reinterpret_cast<double*>(b + L.logits);
+    r.ids = ids;
+    r.wts = wts;
+    r.active = reinterpret_cast<int32_t*>(b + L.active);
+    r.tickets = reinterpret_cast<unsigned*>(b + L.tickets);
+    r.xq = b + L.xq;
+    r.xs = reinterpret_cast<float*>(b + L.xs);
+    const dim3 rgrid(r.log_blocks + cdiv((long long)T * HB, kRouteThreads / 16));
+    cudaError_t e;
+#define I8_ROUTE(TT) \
+    (f16 ? launch(k_moe_route<TT, F16>, rgrid, dim3(kRouteThreads), 0, s, true, r) \
+         : launch(k_moe_route<TT, BF16>, rgrid, dim3(kRouteThreads), 0, s, true, r))
+    e = tt == 1 ? I8_ROUTE(1) : I8_ROUTE(4);
+#undef I8_ROUTE
+    if (e != cudaSuccess) return cuda_status(e);
+
+    Fp8RowsParams p{};
+    p.M = T;
+    p.MB = 1;
+    p.active = r.active;
+    p.ids = ids;
+    p.wts = wts;
+    p.top_k = top_k;
+    p.hq = b + L.hq;
+    p.hs = reinterpret_cast<float*>(b + L.hs);
+    p.parts = reinterpret_cast<float*>(b + L.parts);
+    p.status = reinterpret_cast<int*>(b + L.status);
+    p.wait_limit_ns = o.wait_ns;
+    p.test_flags = o.test_flags;
+    Fp8RowsParams g = p;
+    g.N = I;
+    g.K = H;
+    g.KB = HB;
+    g.NB = IB;
+    g.xs = r.xs;
+    g.ws = w->gate_scales;
+    g.ws2 = w->up_scales;
+    g.tickets = reinterpret_cast<unsigned*>(b + L.t_gate);
+    const int ggrid = fr_shares((long long)A * IB * HB, (long long)A * IB, ctas);
+    e = nt == 16   ? launch_rows<kGateUp, 16, false, F16>(dev, ggrid, tg, tu, tx, g, s, true)
+        : nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, g, s, true)
+                   : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, g, s, true);
+    if (e != cudaSuccess) return cuda_status(e);
+    Fp8RowsParams d = p;
+    d.N = H;
+    d.K = I;
+    d.KB = IB;
+    d.NB = HB;
+    d.xs = p.hs;
+    d.ws = w->down_scales;
+    d.Y = Y;
+    d.test_flags = 0;
+    d.tickets = reinterpret_cast<unsigned*>(b + L.t_down);
+    const int dgrid = fr_shares((long long)A * IB * HB, HB, ctas);
+#define I8_DOWN(NT)                                                                        \
+    (f16 ? launch_rows<kDown, NT, false, F16>(dev, dgrid, td, td, th, d, s, true)          \
+         : launch_rows<kDown, NT, false, BF16>(dev, dgrid, td, td, th, d, s, true))
+    e = nt == 16 ? I8_DOWN(16) : nt == 32 ? I8_DOWN(32) : I8_DOWN(64);
+#undef I8_DOWN
+    return cuda_status(e);
+}
+
+}  // extern "C"

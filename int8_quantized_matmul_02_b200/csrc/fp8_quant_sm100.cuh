@@ -1,0 +1,108 @@
+// Block-scaled e4m3 codes of activations (one scale per row and block of 128
+// consecutive k) and of weights (one scale per 128 x 128 block); the rule is
+// in fp8_common.cuh.
+//
+// Activations: bound by HBM, 2 bytes read and 1 written per value.  A block of
+// 128 16-bit values is 16 lanes x 16 bytes, so a half-warp holds it in
+// registers, takes its maximum with packed 16-bit instructions and four
+// shuffles, and writes 8 codes per lane.  A warp reads 512 consecutive bytes;
+// each half-warp has kQuantBlocks blocks in flight.
+#pragma once
+
+#include "fp8_common.cuh"
+
+namespace i8mm {
+
+constexpr int kQuantBlocks = 4;    // blocks of 128 in flight per half-warp
+constexpr int kQuantThreads = 256;
+
+// Half-warp `hw` of `nhw` takes blocks hw, hw + nhw, ... of the M x KB blocks
+// (row-major).  scale(m, b) goes to scales[m * sm + b * sb].
+template <typename T>
+__device__ __forceinline__ void quant_fp8_blocks(const uint16_t* __restrict__ X, long long nblocks, int K, int KB,
+                                                 uint8_t* __restrict__ codes, float* __restrict__ scales, long long sm,
+                                                 long long sb, long long hw, long long nhw) {
+    const int sub = threadIdx.x & 15;  // this lane's 8 values of the block
+    // every half-warp of a warp runs the same number of rounds: the shuffles
+    // below stay inside a half-warp but name the whole warp
+    const long long first = hw - ((threadIdx.x >> 4) & 1);
+    for (long long w0 = first; w0 < nblocks; w0 += nhw * kQuantBlocks) {
+        const long long b0 = w0 + ((threadIdx.x >> 4) & 1);
+        uint4 x[kQuantBlocks];
+        long long m[kQuantBlocks];
+        int kb[kQuantBlocks];
+        bool in[kQuantBlocks];
+#pragma unroll
+        for (int i = 0; i < kQuantBlocks; ++i) {
+            const long long b = b0 + nhw * i;
+            m[i] = b < nblocks ? b / KB : 0;
+            kb[i] = b < nblocks ? (int)(b - m[i] * KB) : 0;
+            in[i] = b < nblocks && kb[i] * 128 + sub * 8 < K;  // K % 16 == 0: all 8 values or none
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (in[i]) x[i] = __ldg(reinterpret_cast<const uint4*>(X + m[i] * K + kb[i] * 128 + sub * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < kQuantBlocks; ++i) {
+            float a = T::pair_max(fp8_amax8<T>(T::as_pair(0u), x[i]));
+#pragma unroll
+            for (int d = 8; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+            const float s = fp8_block_scale(a);
+            if (in[i]) {
+                *reinterpret_cast<uint2*>(codes + m[i] * K + kb[i] * 128 + sub * 8) =
+                    fp8_codes8<T>(x[i], __frcp_rn(s));
+                if (sub == 0) scales[m[i] * sm + kb[i] * sb] = s;
+            }
+        }
+    }
+}
+
+// grid-stride over the blocks; launched with PDL (it waits before it reads).
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads)
+    k_quant_fp8(const uint16_t* __restrict__ X, long long nblocks, int K, int KB, uint8_t* __restrict__ codes,
+                float* __restrict__ scales, long long sm, long long sb) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long hw = ((long long)blockIdx.x * kQuantThreads + threadIdx.x) >> 4;
+    quant_fp8_blocks<T>(X, nblocks, K, KB, codes, scales, sm, sb, hw, (long long)gridDim.x * (kQuantThreads / 16));
+}
+
+// One 128 x 128 block of a weight per thread block: W is K x N (row-major, 16
+// bits), the codes N x K, scales[n_block * KB + k_block].  Once, at load.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_quant_weight_fp8(const uint16_t* __restrict__ W, int K, int N, uint8_t* __restrict__ codes,
+                       float* __restrict__ scales) {
+    __shared__ uint16_t tile[128][130];  // [k][n]
+    __shared__ float red[8];
+    const int k0 = blockIdx.y * 128, n0 = blockIdx.x * 128;
+    const int nk = min(128, K - k0), nn = min(128, N - n0);
+    float a = 0.0f;
+    for (int i = threadIdx.x; i < 128 * 64; i += 256) {
+        const int k = i >> 6, n = (i & 63) * 2;
+        uint32_t w = 0;
+        if (k < nk && n < nn) w = *reinterpret_cast<const uint32_t*>(W + (size_t)(k0 + k) * N + n0 + n);  // N even
+        tile[k][n] = (uint16_t)w;
+        tile[k][n + 1] = (uint16_t)(w >> 16);
+        a = fmaxf(a, T::pair_max(T::abs_max(T::as_pair(0u), w)));
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, red[i]);
+    const float s = fp8_block_scale(a), inv = __frcp_rn(s);
+    if (threadIdx.x == 0) scales[(size_t)blockIdx.x * gridDim.y + blockIdx.y] = s;
+    for (int i = threadIdx.x; i < 128 * 32; i += 256) {
+        const int n = i >> 5, k = (i & 31) * 4;
+        if (n < nn && k < nk) {
+            const uint32_t q = e4m3x4(__fmul_rn(T::to_float(tile[k][n]), inv), __fmul_rn(T::to_float(tile[k + 1][n]), inv),
+                                      __fmul_rn(T::to_float(tile[k + 2][n]), inv),
+                                      __fmul_rn(T::to_float(tile[k + 3][n]), inv));
+            *reinterpret_cast<uint32_t*>(codes + (size_t)(n0 + n) * K + k0 + k) = q;
+        }
+    }
+}
+
+}  // namespace i8mm

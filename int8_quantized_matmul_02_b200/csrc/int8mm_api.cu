@@ -15,10 +15,14 @@
 #include "int8mm.h"
 #include "codec_kernels.cuh"
 #include "decode_sm100.cuh"
+#include "fp8_gemm_sm100.cuh"
+#include "fp8_quant_sm100.cuh"
+#include "fp8_rows_sm100.cuh"
 #include "gemm2sm_sm100.cuh"
 #include "gemm_grouped_sm100.cuh"
 #include "gemm_sm100.cuh"
 #include "int4_sm100.cuh"
+#include "moe_route_sm100.cuh"
 #include "quant_kernels.cuh"
 
 namespace {
@@ -1322,3 +1326,5 @@ int8mm_status int8mm_forward_grouped(const uint16_t* X, int M, const int8mm_grou
 }
 
 }  // extern "C"
+
+#include "fp8_api.cuh"

@@ -1,0 +1,213 @@
+// The router of the mixture-of-experts layer, in one launch with the
+// quantisation of the tokens' activations (which does not depend on it):
+//
+//   l[t, e] = sum_h X[t, h] R[e, h]         64-bit sums of exact products
+//   p       = softmax over the experts; each token takes its top_k experts
+//             (ties to the lower index); weight p, or p / (sum of the chosen p)
+//
+// The scores are summed in 64 bits because a rounding there can change which
+// expert a token takes, a whole expert's output and not a rounding's worth.
+// The work is small (T * E * H multiply-adds); what bounds the kernel is the
+// chain of its steps.  A block takes 4 experts x kTT tokens; the last block of
+// a token group (a ticket) picks the experts of those tokens, a warp per
+// token, and the last group lists the chosen experts in ascending order.
+#pragma once
+
+#include "fp8_quant_sm100.cuh"
+
+namespace i8mm {
+
+struct RouteParams {
+    const uint16_t* X;       // T x H
+    const uint16_t* R;       // E x H
+    int T, H, E, top_k, renorm;
+    int log_blocks;          // blocks of scores; the rest quantise X
+    double* logits;          // T x E
+    int32_t* ids;            // T x top_k
+    float* wts;              // T x top_k
+    int32_t* active;         // count, then chosen experts
+    unsigned* tickets;       // one per token group and one more, zero between calls
+    uint8_t* xq;             // T x H codes, scales [b * T + t]
+    float* xs;
+};
+
+constexpr int kRouteThreads = 256;
+constexpr int kRouteExperts = 4;     // experts of a score block
+constexpr int kMaxExperts = 256;
+
+// Order-preserving integer of a score: larger score, larger key; -0 as +0; a
+// NaN below every number, so that the choice is always top_k distinct experts.
+__device__ __forceinline__ unsigned long long score_key(double l) {
+    if (l != l) return 0ull;
+    const long long b = __double_as_longlong(l + 0.0);
+    return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
+}
+
+template <int kTT, typename T>
+__global__ void __launch_bounds__(kRouteThreads)
+    k_moe_route(const RouteParams p) {
+    __shared__ double red[kRouteThreads / 32][kRouteExperts * kTT];
+    __shared__ int flags[kMaxExperts];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    if ((int)blockIdx.x >= p.log_blocks) {
+        const int KB = (p.H + 127) / 128;
+        const long long b = (int)blockIdx.x - p.log_blocks, nb = (int)gridDim.x - p.log_blocks;
+        quant_fp8_blocks<T>(p.X, (long long)p.T * KB, p.H, KB, p.xq, p.xs, 1, p.T, (b * kRouteThreads + tid) >> 4,
+                            nb * (kRouteThreads / 16));
+        return;
+    }
+    const int eb = (p.E + kRouteExperts - 1) / kRouteExperts;
+    const int tg = (int)blockIdx.x / eb, e0 = ((int)blockIdx.x % eb) * kRouteExperts, t0 = tg * kTT;
+
+    double acc[kRouteExperts][kTT];
+#pragma unroll
+    for (int i = 0; i < kRouteExperts; ++i)
+#pragma unroll
+        for (int j = 0; j < kTT; ++j) acc[i][j] = 0.0;
+    for (int c = tid; c < p.H / 8; c += kRouteThreads) {
+        uint4 r[kRouteExperts], x[kTT];
+#pragma unroll
+        for (int i = 0; i < kRouteExperts; ++i)
+            r[i] = e0 + i < p.E ? __ldg(reinterpret_cast<const uint4*>(p.R + (size_t)(e0 + i) * p.H) + c)
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kTT; ++j)
+            x[j] = t0 + j < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + (size_t)(t0 + j) * p.H) + c)
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            double xa[kTT], xb[kTT];
+#pragma unroll
+            for (int j = 0; j < kTT; ++j) {
+                const float2 f = T::to_float2(reinterpret_cast<const uint32_t*>(&x[j])[w]);
+                xa[j] = f.x;
+                xb[j] = f.y;
+            }
+#pragma unroll
+            for (int i = 0; i < kRouteExperts; ++i) {
+                const float2 f = T::to_float2(reinterpret_cast<const uint32_t*>(&r[i])[w]);
+                const double ra = f.x, rb = f.y;
+#pragma unroll
+                for (int j = 0; j < kTT; ++j) acc[i][j] = fma(rb, xb[j], fma(ra, xa[j], acc[i][j]));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRouteExperts; ++i)
+#pragma unroll
+        for (int j = 0; j < kTT; ++j) {
+            double a = acc[i][j];
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+            if (lane == 0) red[warp][i * kTT + j] = a;
+        }
+    __syncthreads();
+    if (tid < kRouteExperts * kTT) {
+        const int e = e0 + tid / kTT, t = t0 + tid % kTT;
+        double a = 0.0;
+#pragma unroll
+        for (int w = 0; w < kRouteThreads / 32; ++w) a += red[w][tid];
+        if (e < p.E && t < p.T) __stcg(p.logits + (size_t)t * p.E + e, a);
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const bool last = atomicAdd(&p.tickets[tg], 1u) == (unsigned)(eb - 1);
+        if (last) p.tickets[tg] = 0;
+        s_last = last;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+
+    // the experts of token t0 + warp
+    if (warp < kTT && t0 + warp < p.T) {
+        const int t = t0 + warp;
+        constexpr int kPer = kMaxExperts / 32;
+        double l[kPer];
+        unsigned long long key[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane + 32 * i;
+            l[i] = e < p.E ? __ldcg(p.logits + (size_t)t * p.E + e) : 0.0;
+            key[i] = score_key(l[i]);
+        }
+        unsigned gone = 0;  // this lane's experts already chosen (or past E)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (lane + 32 * i >= p.E) gone |= 1u << i;
+        double top = 0.0;       // the largest score
+        float mine = 0.0f;      // lane j: e^(l - top) of choice j
+        int mine_id = 0;
+        for (int j = 0; j < p.top_k; ++j) {
+            unsigned long long best = 0;
+            int at = kMaxExperts;
+#pragma unroll
+            for (int i = kPer - 1; i >= 0; --i)  // downwards: an equal key at a lower index wins
+                if (!((gone >> i) & 1u) && key[i] >= best) {
+                    best = key[i];
+                    at = lane + 32 * i;
+                }
+            const unsigned hi = __reduce_max_sync(0xffffffffu, at < kMaxExperts ? (unsigned)(best >> 32) : 0u);
+            const bool in_hi = at < kMaxExperts && (unsigned)(best >> 32) == hi;
+            const unsigned lo = __reduce_max_sync(0xffffffffu, in_hi ? (unsigned)best : 0u);
+            const int e = (int)__reduce_min_sync(
+                0xffffffffu, in_hi && (unsigned)best == lo ? (unsigned)at : (unsigned)kMaxExperts);
+            double le = 0.0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i == e) {
+                    gone |= 1u << i;
+                    le = l[i];
+                }
+            le = __shfl_sync(0xffffffffu, le, e & 31);
+            if (j == 0) top = le;
+            if (lane == j) {
+                mine = expf((float)(le - top));
+                mine_id = e;
+            }
+        }
+        float sum = 0.0f;
+        if (p.renorm) {
+            sum = lane < p.top_k ? mine : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < p.E) sum += expf((float)(l[i] - top));
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane < p.top_k) {
+            __stcg(p.ids + (size_t)t * p.top_k + lane, mine_id);
+            __stcg(p.wts + (size_t)t * p.top_k + lane, __fdiv_rn(mine, sum));
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    const int groups = (p.T + kTT - 1) / kTT;
+    if (tid == 0) {
+        const bool last = atomicAdd(&p.tickets[groups], 1u) == (unsigned)(groups - 1);
+        if (last) p.tickets[groups] = 0;
+        s_last = last;
+    }
+    for (int e = tid; e < kMaxExperts; e += kRouteThreads) flags[e] = 0;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int i = tid; i < p.T * p.top_k; i += kRouteThreads) flags[__ldcg(p.ids + i)] = 1;
+    __syncthreads();
+    if (warp == 0) {
+        int n = 0;
+        for (int e = lane; e < kMaxExperts; e += 32) {
+            const unsigned m = __ballot_sync(0xffffffffu, flags[e] != 0);
+            if (flags[e]) p.active[1 + n + __popc(m & ((1u << lane) - 1u))] = e;
+            n += __popc(m);
+        }
+        if (lane == 0) p.active[0] = n;
+    }
+}
+
+}  // namespace i8mm
