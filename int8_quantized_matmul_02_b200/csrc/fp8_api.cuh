@@ -24,6 +24,10 @@ Fp8Layout fp8_weight_layout(int K, int N) {
     return L;
 }
 
+// Rows of the scales of X in the workspace (a block's scales are contiguous):
+// whole tiles of the tiled kernel, which reads four rows at a time and past M.
+long long fp8_pitch(int M) { return ((long long)M + 255) / 256 * 256; }
+
 struct Fp8WsLayout {
     size_t status, codes, scales, tickets, parts, total;
 };
@@ -34,7 +38,7 @@ Fp8WsLayout fp8_ws_layout(int M, int K, int N) {
     L.codes = o;
     o = align_up(o + (size_t)M * K, 256);
     L.scales = o;
-    o = align_up(o + (size_t)M * cdiv(K, 128) * 4, 256);
+    o = align_up(o + (size_t)fp8_pitch(M) * cdiv(K, 128) * 4, 256);
     L.tickets = o;
     L.parts = o;
     if (M <= kFp8RowsMaxM) {
@@ -99,12 +103,31 @@ bool make_map3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Opt in to a kernel's shared memory once per device.
-template <auto Kern>
+// Y (M x N, 16 bits) in boxes of 32 rows x 32 columns with the 64-byte swizzle.
+bool make_map_y(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t N, uint64_t M) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {N, M};
+    cuuint64_t strides[1] = {N * 2};
+    cuuint32_t box[2] = {32, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Opt in to a kernel's shared memory once per device, and refuse a kernel
+// whose launch holds fewer registers than its setmaxnreg split hands out.
+template <auto Kern, int kMinRegs = 0>
 cudaError_t fp8_opt_in(int dev, int smem) {
     static std::atomic<uint64_t> done{0};  // one bit per device (current_device admits fewer than 64)
     if ((done.load(std::memory_order_acquire) >> dev) & 1u) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && kMinRegs > 0) {
+        cudaFuncAttributes a{};
+        e = cudaFuncGetAttributes(&a, Kern);
+        if (e == cudaSuccess && a.numRegs < kMinRegs) e = cudaErrorInvalidConfiguration;
+    }
     if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
     return e;
 }
@@ -129,13 +152,13 @@ cudaError_t launch_rows(int dev, int grid, const CUtensorMap& tw, const CUtensor
     static_assert(smem <= kMaxSmemOptin, "shared memory of one SM");
     cudaError_t e = fp8_opt_in<k_fp8_rows<kMode, kNT, kFuse, T>>(dev, smem);
     if (e != cudaSuccess) return e;
-    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(kFRThreads), smem, s, pdl, tw, tw2, tx, p);
+    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kMode, kNT>()), smem, s, pdl, tw, tw2, tx, p);
 }
 
 template <int kBN, typename T>
 cudaError_t launch_gemm_fp8(int dev, int grid, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
                             const Fp8GemmParams& p, cudaStream_t s, bool pdl) {
-    cudaError_t e = fp8_opt_in<k_gemm_fp8_2sm<kBN, T>>(dev, f8_smem_bytes(kBN));
+    cudaError_t e = fp8_opt_in<k_gemm_fp8_2sm<kBN, T>, kF8LaunchRegs>(dev, f8_smem_bytes(kBN));
     if (e != cudaSuccess) return e;
     return launch_ex(k_gemm_fp8_2sm<kBN, T>, dim3(grid), dim3(kF8Threads), f8_smem_bytes(kBN), s, pdl, 2, ta, tb, ty, p);
 }
@@ -245,7 +268,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
     const int nt = fp8_rows_nt(M);
     const bool fuse = rows && nt <= 32;
     cudaError_t e = cudaSuccess;
-    if (!fuse) e = launch_quant_fp8(X, dtype, M, K, xq, xs, 1, M, info->sm_count, s);
+    if (!fuse) e = launch_quant_fp8(X, dtype, M, K, xq, xs, 1, fp8_pitch(M), info->sm_count, s);
     if (e != cudaSuccess) return cuda_status(e);
     CUtensorMap ta, tb;
     if (rows) {
@@ -258,6 +281,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         p.MB = cdiv(M, nt);
         p.X = X;
         p.xs = xs;
+        p.xs_pitch = fp8_pitch(M);
         p.ws = w->scales;
         p.Y = Y;
         p.parts = reinterpret_cast<float*>(b + L.parts);
@@ -283,8 +307,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         CUtensorMap ty;
         if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, 128) ||
             !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, bn / 2) ||
-            !make_map(&ty, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
-                      (uint64_t)N * 2, 64, 32))
+            !make_map_y(&ty, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M))
             return INT8MM_ERR_CUDA;
         Fp8GemmParams p{};
         p.M = M;
@@ -298,7 +321,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         const int fit = (int)std::min<uint64_t>(1u << 20, (48ull << 20) / ((uint64_t)kF8BM * (uint64_t)K));
         p.group_m = std::min(std::max(8, fit), p.num_m_blocks);
         p.xs = xs;
-        p.xs_pitch = M;
+        p.xs_pitch = fp8_pitch(M);
         p.ws = w->scales;
         p.status = reinterpret_cast<int*>(b + L.status);
         p.wait_limit_ns = o.wait_ns;
@@ -399,6 +422,7 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     g.KB = HB;
     g.NB = IB;
     g.xs = r.xs;
+    g.xs_pitch = T;
     g.ws = w->gate_scales;
     g.ws2 = w->up_scales;
     g.tickets = reinterpret_cast<unsigned*>(b + L.t_gate);
@@ -413,6 +437,7 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     d.KB = IB;
     d.NB = HB;
     d.xs = p.hs;
+    d.xs_pitch = T;
     d.ws = w->down_scales;
     d.Y = Y;
     d.test_flags = 0;

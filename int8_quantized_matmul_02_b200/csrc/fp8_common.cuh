@@ -90,22 +90,43 @@ __device__ __forceinline__ typename T::pair fp8_amax8(typename T::pair m, uint4 
     return T::abs_max(T::abs_max(T::abs_max(T::abs_max(m, x.x), x.y), x.z), x.w);
 }
 
-// wait_bounded / wait_bounded_cluster without a call, for threads that hold
-// most of their registers live across the wait.
-template <bool kCluster>
-__device__ __forceinline__ bool wait_bounded_inline(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+// wait_bounded for the waits that the pace of a kernel hangs on: no call (the
+// caller may hold most of its registers live), and no look at the timer until
+// the wait has polled for a while (a timer read between polls delays the
+// moment at which a completed phase is seen).  CTA-scope acquire also for
+// barriers that the pair's other CTA or the tensor core arrives on: what they
+// order is TMEM and the async proxy, through tcgen05 fences, and no ordinary
+// memory of the other CTA is read after them.
+__device__ __forceinline__ bool wait_fast(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-            if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+            if (mbar_try_wait(bar, parity)) return true;
         if (*c.abort_flag) return false;
         if (globaltimer_ns() - t0 > c.limit_ns) {
             raise_abort(c);
             return false;
         }
+    }
+}
+
+// wait_drain and settle_after_abort without a call (a kernel that splits its
+// registers with setmaxnreg makes none).
+__device__ __forceinline__ void wait_drain_inline(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > limit_ns) return;
+}
+__device__ __forceinline__ void settle_inline() {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (globaltimer_ns() - t0 < 200ull * 1000) {
     }
 }
 

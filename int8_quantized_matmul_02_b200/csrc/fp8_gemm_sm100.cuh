@@ -6,17 +6,27 @@
 //
 // The scales change every 128 k and are not powers of two, so a block's sum
 // has to leave the tensor cores before the next block is added: every 128 k
-// the accumulator is read back and added to running sums in registers.  Two
-// TMEM accumulators alternate, so that this runs beside the next block's MMAs.
-// What it costs per block and SM: a 128 x kBN tile is 128 * kBN FMAs against
-// 128 * kBN * 128 MACs, and a column of TMEM words per lane quadrant and FMA.
-// The 256 x 256 pair tile (a row of 128 columns per epilogue thread) is the
-// largest whose sums fit the registers: 128 sums and 32 columns being added
-// per thread.  It also halves the operand bytes that a pair stages per MAC
-// against 256 x 128.
+// the accumulator is read back and added to running sums in registers, two
+// columns per instruction.  Two TMEM accumulators alternate, so that this runs
+// beside the next block's MMAs.
+//
+// What bounds it is the way round that one accumulator takes: MMAs (565
+// cycles a block), completion seen by the epilogue (~450), reading it back and
+// adding (~300), release seen by the issuing thread (~220), issue (~150).
+// With two accumulators a block takes half of that, ~850 cycles, against the
+// MMAs' 565; TMEM (512 columns) holds no third.  Measured and not kept, for
+// 4096 x 12288 x 49152 (as built: 2.22 ms): the two column halves as separate
+// accumulators of 128 columns (2.48 ms: MMAs of N = 128 run at a lower rate);
+// 16 epilogue warps of 64 columns (2.41 ms: more threads to see the
+// completion and to release); the scale products made by two other warps
+// (2.58 ms: the scale is read after the completion instead of before).
+// The 256 x 256 pair tile is the largest whose sums fit the registers: 128
+// sums and two loads of 32 columns per thread, with the register file split by
+// setmaxnreg.
 //   warp 0      TMA producer (both CTAs; completion on the even CTA's barrier);
 //   warp 1      TMEM allocation (512 columns) and, in the even CTA, MMA issue;
-//   warps 2-9   epilogue: TMEM lane quadrant w % 4, column half (w - 2) / 4.
+//   warps 2-3   idle (they complete the group of four that gives up registers);
+//   warps 4-11  epilogue: TMEM lane quadrant w % 4, column half (w - 4) / 4.
 // The scales of the next four blocks are copied to shared memory ahead of use
 // (cp.async, one group per block); half of a tile's columns lie in one block
 // of 128 channels, so a thread needs one xs and one ws per block.
@@ -30,7 +40,7 @@ namespace i8mm {
 struct Fp8GemmParams {
     int M, N, KB;                  // KB = ceil(K / 128)
     int num_m_blocks, num_n_blocks, num_tiles, group_m;
-    const float* xs;               // KB x xs_pitch: xs[b * xs_pitch + m]
+    const float* xs;               // KB x xs_pitch: xs[b * xs_pitch + m]; the pitch is a multiple of 256
     long long xs_pitch;
     const float* ws;               // ceil(N / 128) x KB
     int* status;
@@ -41,14 +51,18 @@ struct Fp8GemmParams {
 constexpr int kF8BM = 256;
 constexpr int kF8Stages = 5;
 constexpr int kF8EpiWarps = 8;
-constexpr int kF8Threads = 64 + 32 * kF8EpiWarps;
+constexpr int kF8Threads = 128 + 32 * kF8EpiWarps;
+constexpr int kF8EpiRegs = 232, kF8CtlRegs = 40;  // registers per thread after the split
+constexpr int kF8LaunchRegs = 168;                // and before it
+static_assert(kF8EpiWarps * kF8EpiRegs + 4 * kF8CtlRegs <= (kF8EpiWarps + 4) * kF8LaunchRegs, "register split");
 constexpr int kF8Ahead = 4;        // blocks whose scales are fetched ahead
 constexpr int kF8Slots = 2 * kF8Ahead;
 constexpr int kF8ScaleBytes = kF8Slots * (32 + 4) * 4;  // per epilogue warp
+constexpr int kF8EpiBufBytes = 32 * 64;           // 32 rows x 32 16-bit columns
 
 __host__ __device__ constexpr int f8_stage_bytes(int bn) { return 128 * 128 + (bn / 2) * 128; }
 __host__ __device__ constexpr int f8_smem_bytes(int bn) {
-    return 1024 + kF8Stages * f8_stage_bytes(bn) + kF8EpiWarps * (kGemmEpiBufBytes + kF8ScaleBytes) + 256;
+    return 1024 + kF8Stages * f8_stage_bytes(bn) + kF8EpiWarps * (kF8EpiBufBytes + kF8ScaleBytes) + 256;
 }
 static_assert(f8_smem_bytes(256) <= 232448, "shared memory of one SM");
 
@@ -63,33 +77,43 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// v[0..31] += acc[0..31] * s, two lanes per instruction.
-__device__ __forceinline__ void fma32(float* v, const uint32_t (&r)[32], float s) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        asm("{\n\t.reg .b64 x, y, z;\n\t"
-            "mov.b64 x, {%2, %3};\n\t"
-            "mov.b64 y, {%4, %4};\n\t"
-            "mov.b64 z, {%0, %1};\n\t"
-            "fma.rn.f32x2 z, x, y, z;\n\t"
-            "mov.b64 {%0, %1}, z;\n\t}"
-            : "+f"(v[i]), "+f"(v[i + 1])
-            : "f"(__uint_as_float(r[i])), "f"(__uint_as_float(r[i + 1])), "f"(s));
+// Running sums are kept as pairs in 64-bit registers: an fma.rn.f32x2 on
+// separate 32-bit sums costs moves into and out of register pairs (measured:
+// 357 instructions per warp and block against the FMAs' 64).
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f32x2_parts(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
 
-// 32 fp32 values of one row to 16 bits, into half of the row's 128-byte line
-// of a staging buffer with the 128-byte swizzle.
+// v[0..15] (32 sums) += acc[0..31] * s.
+__device__ __forceinline__ void fma32(uint64_t* v, const uint32_t (&r)[32], uint64_t s2) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        fma_f32x2(v[i], f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2);
+}
+
+// 32 fp32 values of one row to 16 bits, into the row's 64-byte line of a
+// staging buffer with the 64-byte swizzle.
 template <typename T>
-__device__ __forceinline__ void stage_row32_t(uint8_t* buf, int row, int half32, const float* v) {
+__device__ __forceinline__ void stage_row32_t(uint8_t* buf, int row, const uint64_t* v) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        uint4 w;
-        w.x = T::pack(v[8 * c + 0], v[8 * c + 1]);
-        w.y = T::pack(v[8 * c + 2], v[8 * c + 3]);
-        w.z = T::pack(v[8 * c + 4], v[8 * c + 5]);
-        w.w = T::pack(v[8 * c + 6], v[8 * c + 7]);
-        const int chunk = half32 * 4 + c;
-        *reinterpret_cast<uint4*>(buf + row * 128 + ((chunk ^ (row & 7)) << 4)) = w;
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = f32x2_parts(v[4 * c + i]);
+            h[i] = T::pack(f.x, f.y);
+        }
+        *reinterpret_cast<uint4*>(buf + row * 64 + ((c ^ ((row >> 1) & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
 
@@ -103,8 +127,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = smem;
     uint8_t* epi = smem + kF8Stages * kStageBytes;
-    float* sscale = reinterpret_cast<float*>(epi + kF8EpiWarps * kGemmEpiBufBytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(epi + kF8EpiWarps * (kGemmEpiBufBytes + kF8ScaleBytes));
+    float* sscale = reinterpret_cast<float*>(epi + kF8EpiWarps * kF8EpiBufBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(epi + kF8EpiWarps * (kF8EpiBufBytes + kF8ScaleBytes));
     uint64_t* full = bars;                    // [stages] even CTA: both CTAs' bytes
     uint64_t* empty = bars + kF8Stages;       // [stages] each CTA: its stage is free
     uint64_t* tfull = bars + 2 * kF8Stages;   // [2] each CTA: a block's sums are ready
@@ -156,7 +180,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     pdl_wait();  // the codes and scales of X come from the kernel before
     pdl_launch_dependents();
 
-    if (warp < 2) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8CtlRegs));
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
             if (elect_one()) {
@@ -171,7 +196,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                     const int row_a = mb * kF8BM + (int)rank * 128;
                     const int row_b = nb * kBN + (int)rank * (kBN / 2);
                     for (int kb = 0; kb < p.KB; ++kb) {
-                        if (!wait_bounded_cluster(&empty[stage], phase ^ 1, wctx)) {
+                        if (!wait_fast(&empty[stage], phase ^ 1, wctx)) {
                             ok = false;
                             break;
                         }
@@ -187,128 +212,139 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                     }
                 }
             }
-        } else {
+        } else if (warp == 1) {
             // ------------------------------------------------ MMA issuer (even CTA)
             if (rank == 0 && elect_one()) {
                 const uint32_t idesc = idesc_e4m3_f32(kF8BM, kBN);
-                int stage = 0, acc = 0;
-                uint32_t phase = 0, acc_phase = 0;
-                bool ok = true, issued = false;
-                for (int tile = cid; tile < p.num_tiles && ok; tile += ncl) {
-                    for (int kb = 0; kb < p.KB; ++kb) {
-                        if (!wait_bounded_cluster(&tempty[acc], acc_phase ^ 1, wctx) ||
-                            !wait_bounded(&full[stage], phase, wctx)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t sa = smem_u32(ring + stage * kStageBytes);
-                        mma_e4m3_k128_2sm(tmem_base + (uint32_t)(acc * 256), sdesc_k128sw(sa),
-                                          sdesc_k128sw(sa + 128 * 128), idesc);
-                        issued = true;
-                        tc_commit_pair(&empty[stage]);
-                        if (!((p.test_flags & 1u) && tile == cid && kb == 0)) tc_commit_pair(&tfull[acc]);
-                        if (++stage == kF8Stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
-                        acc ^= 1;
-                        acc_phase ^= (acc == 0);
+                int stage = 0;
+                uint32_t phase = 0;
+                bool issued = false;
+                const uint32_t blocks = (uint32_t)((p.num_tiles - cid + ncl - 1) / ncl) * (uint32_t)p.KB;
+                // a look at a barrier takes ~170 cycles while the tensor core reads
+                // shared memory, so the next stage's is taken during this block's issue
+                bool loaded = false;
+                for (uint32_t q = 0; q < blocks; ++q) {
+                    const uint32_t acc = q & 1;
+                    if (!wait_fast(&tempty[acc], ((q >> 1) & 1) ^ 1, wctx)) break;
+                    if (!loaded && !wait_fast(&full[stage], phase, wctx)) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + stage * kStageBytes);
+                    mma_e4m3_k128_2sm(tmem_base + acc * 256, sdesc_k128sw(sa), sdesc_k128sw(sa + 128 * 128), idesc);
+                    issued = true;
+                    if (!((p.test_flags & 1u) && q == 0)) tc_commit_pair(&tfull[acc]);
+                    tc_commit_pair(&empty[stage]);
+                    if (++stage == kF8Stages) {
+                        stage = 0;
+                        phase ^= 1;
                     }
+                    loaded = mbar_try_wait(&full[stage], phase);
                 }
                 if (issued) {  // every pair MMA has retired before TMEM is freed
                     tc_commit_pair(drain);
-                    wait_drain(drain, 0, kDrainLimitNs);
+                    wait_drain_inline(drain, 0, kDrainLimitNs);
                 }
             }
         }
     } else {
-        // ------------------------------------------------ epilogue (warps 2..9, both CTAs)
-        const int ew = warp - 2;
+        // ------------------------------------------------ epilogue (warps 4..11, both CTAs)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
+        const int ew = warp - 4;
         const int quad = warp & 3, half = ew >> 2;
-        uint8_t* buf = epi + ew * kGemmEpiBufBytes;
+        uint8_t* buf = epi + ew * kF8EpiBufBytes;
         float* slots = sscale + ew * (kF8ScaleBytes / 4);  // [slots] of 32 xs and one ws (padded to 36)
         const uint32_t tempty0 = map_to_rank(&tempty[0], 0), tempty1 = map_to_rank(&tempty[1], 0);
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        uint32_t fetched = 0, used = 0;  // running counts of scale groups
+        const uint32_t tcol = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * kCols);
+        uint32_t fetched = 0;  // scale groups so far
+        uint32_t q = 0;        // blocks so far: accumulator q & 1
         bool ok = true;
-        // scales of the kb-th block from a tile's start to the next slot (an
-        // empty group past the last tile)
-        const auto fetch = [&](int tile, int kb) {
-            while (kb >= p.KB && tile < p.num_tiles) {  // on into this pair's next tiles
-                kb -= p.KB;
-                tile += ncl;
-            }
-            if (tile < p.num_tiles) {
-                int mb, nb;
-                coords(tile, mb, nb);
-                const int row = mb * kF8BM + (int)rank * 128 + quad * 32 + lane;
-                const int nblk = (nb * kBN + half * kCols) >> 7;
-                float* s = slots + (fetched & (kF8Slots - 1)) * 36;
-                const bool row_in = row < p.M, blk_in = nblk * 128 < p.N;
-                const float* src = p.xs + (row_in ? (size_t)kb * p.xs_pitch + row : 0);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(s + lane)), "l"(src),
-                             "r"(row_in ? 4 : 0)
-                             : "memory");
-                if (lane == 0) {
-                    const float* sw = p.ws + (blk_in ? (size_t)nblk * p.KB + kb : 0);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(s + 32)), "l"(sw),
-                                 "r"(blk_in ? 4 : 0)
-                                 : "memory");
+        // the stream of scales: tile, block and source of the next fetch
+        int ft = cid - ncl, fk = p.KB;
+        const float *fx = nullptr, *fw = nullptr;
+        int fw_bytes = 0;
+        // the next block's scales to the next slot (an empty group past the last tile)
+        const auto fetch = [&]() {
+            if (fk == p.KB) {
+                ft += ncl;
+                fk = 0;
+                if (ft < p.num_tiles) {
+                    int mb, nb;
+                    coords(ft, mb, nb);
+                    const int nblk = (nb * kBN + half * kCols) >> 7;
+                    fx = p.xs + mb * kF8BM + (int)rank * 128 + quad * 32 + lane;  // rows past M: in the pitch, unused
+                    fw_bytes = nblk * 128 < p.N ? 4 : 0;
+                    fw = p.ws + (fw_bytes ? (size_t)nblk * p.KB : 0);
                 }
+            }
+            if (ft < p.num_tiles) {
+                float* s = slots + (fetched & (kF8Slots - 1)) * 36;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s + lane)), "l"(fx) : "memory");
+                if (lane == 0)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(s + 32)), "l"(fw),
+                                 "r"(fw_bytes)
+                                 : "memory");
+                fx += p.xs_pitch;
+                ++fw;
+                ++fk;
             }
             ++fetched;
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll
-        for (int i = 0; i < kF8Ahead; ++i) fetch(cid, i);
+        for (int i = 0; i < kF8Ahead; ++i) fetch();
         for (int tile = cid; tile < p.num_tiles && ok; tile += ncl) {
-            int mb, nb;
-            coords(tile, mb, nb);
-            const int row0 = mb * kF8BM + (int)rank * 128 + quad * 32;
-            const int colw = nb * kBN + half * kCols;
-            float v[kCols];
+            uint64_t v[kCols / 2];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
-            for (int kb = 0; kb < p.KB; ++kb) {
-                fetch(tile, kb + kF8Ahead);
+            for (int i = 0; i < kCols / 2; ++i) v[i] = 0;
+            for (int kb = 0; kb < p.KB; ++kb, ++q) {
+                fetch();
                 asm volatile("cp.async.wait_group %0;" ::"n"(kF8Ahead) : "memory");
                 __syncwarp();
-                const float* s = slots + (used & (kF8Slots - 1)) * 36;
-                const float sc = __fmul_rn(s[lane], s[32]);
-                ++used;
-                if (!__all_sync(0xffffffffu, wait_bounded_inline<true>(&tfull[acc], acc_phase, wctx))) {
+                const float* sl = slots + (q & (kF8Slots - 1)) * 36;
+                const float s1 = __fmul_rn(sl[lane], sl[32]);
+                const uint64_t s = f32x2(s1, s1);
+                if (!__all_sync(0xffffffffu, wait_fast(&tfull[q & 1], (q >> 1) & 1, wctx))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * 256 + half * kCols);
-                uint32_t r[32];
+                const uint32_t t = tcol + ((q & 1) << 8);
+                const auto release = [&]() {  // the accumulator is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                         (q & 1) ? tempty1 : tempty0)
+                                     : "memory");
+                };
+                // one load of 32 columns in flight beside the FMAs of the 32 before
+                uint32_t ra[32], rb[32];
+                tmem_ld32(t, ra);
+                tmem_wait_ld32(ra);
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    tmem_ld32(t + c, r);
-                    tmem_wait_ld32(r);
-                    if (c + 32 == kCols) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)  // the accumulator is free
-                            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                             acc ? tempty1 : tempty0)
-                                         : "memory");
+                for (int c = 0; c < kCols; c += 64) {
+                    tmem_ld32(t + c + 32, rb);
+                    fma32(v + c / 2, ra, s);
+                    tmem_wait_ld32(rb);
+                    if (c + 64 < kCols) {
+                        tmem_ld32(t + c + 64, ra);
+                        fma32(v + c / 2 + 16, rb, s);
+                        tmem_wait_ld32(ra);
+                    } else {
+                        release();
+                        fma32(v + c / 2 + 16, rb, s);
                     }
-                    fma32(v + c, r, sc);
                 }
-                acc ^= 1;
-                acc_phase ^= (acc == 0);
             }
             if (!ok) break;
+            int mb, nb;
+            coords(tile, mb, nb);
+            const int row0 = mb * kF8BM + (int)rank * 128 + quad * 32;
+            const int colw = nb * kBN + half * kCols;
 #pragma unroll
-            for (int c = 0; c < kCols; c += 64) {
+            for (int c = 0; c < kCols; c += 32) {
                 if (lane == 0) bulk_wait_read<0>();  // the buffer's last store has read it
                 __syncwarp();
-                stage_row32_t<TOut>(buf, lane, 0, v + c);
-                stage_row32_t<TOut>(buf, lane, 1, v + c + 32);
+                stage_row32_t<TOut>(buf, lane, v + c / 2);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -322,7 +358,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         __syncwarp();
     }
 
-    if (threadIdx.x == 0 && *abort_flag) settle_after_abort();  // copies issued before the abort land first
+    if (threadIdx.x == 0 && *abort_flag) settle_inline();  // copies issued before the abort land first
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // the even CTA's MMAs no longer read this CTA's shared memory or TMEM

@@ -32,15 +32,16 @@
 //
 //   warp 0     TMA producer of the weight boxes (and of B unless kFuse);
 //   warp 1     TMEM allocation and MMA issue;
-//   warps 2-5  epilogue, TMEM lane quadrant w % 4;
-//   warps 6-9  every fourth unit each: the unit's scale products into shared
+//   warps 2-5  every fourth unit each: the unit's scale products into shared
 //              memory, and with kFuse the rows' codes (the rows' 16-bit values
-//              are read, quantised and written to the swizzled B operand).
+//              are read, quantised and written to the swizzled B operand);
+//   warps 6-   epilogue, TMEM lane quadrant w % 4: four warps, or eight with
+//              half of the rows each where a thread would have to hold more
+//              than 64 sums (128 of them spilled: 85 us for 100 x 11008 x 4096).
 #pragma once
 
 #include "fp8_common.cuh"
 #include "fp8_gemm_sm100.cuh"
-#include "gemm_grouped_sm100.cuh"
 
 namespace i8mm {
 
@@ -54,7 +55,8 @@ struct Fp8RowsParams {
     int NB;                // ceil(N / 128)
     int MB;                // kRows: ceil(M / kNT) row blocks; else 1
     const uint16_t* X;     // kFuse: M x K
-    const float* xs;       // else: scale of row m, block b at [b * M + m]; kDown: [(a * KB + b) * M + m]
+    const float* xs;       // else: scale of row m, block b at [b * xs_pitch + m]; kDown: [(a * KB + b) * xs_pitch + m]
+    long long xs_pitch;
     const float* ws;       // NB x KB (kGateUp, kDown: per expert)
     const float* ws2;      // kGateUp: the up weight's
     const int32_t* active; // kGateUp, kDown: count, then the chosen experts in ascending order
@@ -64,14 +66,13 @@ struct Fp8RowsParams {
     void* Y;               // kRows, kDown: M x N, 16 bits
     uint8_t* hq;           // kGateUp: codes [a][M][N], scales [(a * NB + nb) * M + m]
     float* hs;
-    float* parts;          // two slots of (kA * kNT) x 128 floats per CTA
+    float* parts;          // two slots of kA x kNT x 128 floats per CTA
     unsigned* tickets;     // one per tile, zero between calls
     int* status;
     uint64_t wait_limit_ns;
     uint32_t test_flags;   // bit 0: block 0 never signals its first accumulator (timeout test)
 };
 
-constexpr int kFRThreads = 320;
 constexpr int kFRBufs = 4;       // TMEM accumulators in rotation
 constexpr int kFRSideWarps = 4;
 constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
@@ -79,6 +80,10 @@ constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace
 
 template <int kMode>
 __host__ __device__ constexpr int fr_a() { return kMode == kGateUp ? 2 : 1; }
+template <int kMode, int kNT>
+__host__ __device__ constexpr int fr_epi_warps() { return fr_a<kMode>() * kNT > 64 ? 8 : 4; }
+template <int kMode, int kNT>
+__host__ __device__ constexpr int fr_threads() { return 32 * (2 + kFRSideWarps + fr_epi_warps<kMode, kNT>()); }
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stage_bytes() { return fr_a<kMode>() * 16384 + kNT * 128; }
 template <int kMode, int kNT>
@@ -105,14 +110,17 @@ __host__ __device__ __forceinline__ int fr_shares(long long units, long long til
 }
 
 template <int kMode, int kNT, bool kFuse, typename T>
-__global__ void __launch_bounds__(kFRThreads, 1)
+__global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
     k_fp8_rows(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_w2,
                const __grid_constant__ CUtensorMap tm_x, const Fp8RowsParams p) {
     constexpr int kA = fr_a<kMode>();
     constexpr int kStageBytes = fr_stage_bytes<kMode, kNT>();
     constexpr int kStages = fr_stages<kMode, kNT>();
     constexpr int kSlots = kStages + kFRBufs;
-    constexpr int kCols = kA * kNT;  // running sums per thread
+    constexpr int kCols = kA * kNT;  // columns of an accumulator
+    constexpr int kEpi = fr_epi_warps<kMode, kNT>(), kEpiThreads = 32 * kEpi;
+    constexpr int kRowsT = kNT / (kEpi / 4);  // rows per epilogue thread
+    constexpr int kSums = kA * kRowsT;        // running sums per epilogue thread
     constexpr uint32_t kTmemCols = kFRBufs * kCols < 32 ? 32 : kFRBufs * kCols;
     static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
     extern __shared__ uint8_t smem_raw[];
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kFRThreads, 1)
         }
         for (int b = 0; b < kFRBufs; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 4);
+            mbar_init(&tempty[b], kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kFRThreads, 1)
             uint32_t phase = 0;
             int tile = (int)(u0 / kbt), kb = (int)(u0 - (long long)tile * kbt);
             for (long long u = u0; u < u1; ++u) {
-                if (!wait_bounded(&empty[stage], phase ^ 1, wctx)) break;
+                if (!wait_fast(&empty[stage], phase ^ 1, wctx)) break;
                 uint8_t* sa = ring + stage * kStageBytes;
                 uint8_t* sb = sa + kA * 16384;
                 mbar_arrive_expect_tx(&full[stage], kFuse ? kA * 16384 : kStageBytes);
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kFRThreads, 1)
             uint32_t phase = 0, buf_phase = 0;
             bool issued = false;
             for (long long u = u0; u < u1; ++u) {
-                if (!wait_bounded(&tempty[buf], buf_phase ^ 1, wctx) || !wait_bounded(&full[stage], phase, wctx))
+                if (!wait_fast(&tempty[buf], buf_phase ^ 1, wctx) || !wait_fast(&full[stage], phase, wctx))
                     break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(ring + stage * kStageBytes);
@@ -245,10 +253,11 @@ __global__ void __launch_bounds__(kFRThreads, 1)
                 wait_drain(drain, 0, kDrainLimitNs);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp >= 2 + kFRSideWarps) {
         // ------------------------------------------------ epilogue
         const int quad = warp & 3, ch = quad * 32 + lane;
-        const int et = (int)threadIdx.x - 64;  // 0..127
+        const int et = (int)threadIdx.x - 32 * (2 + kFRSideWarps);  // 0 .. kEpiThreads - 1
+        const int r0 = (et >> 7) * kRowsT;                           // this thread's first row
         int buf = 0, slot = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
@@ -258,43 +267,48 @@ __global__ void __launch_bounds__(kFRThreads, 1)
             const long long t0 = (long long)tile * kbt, t1 = t0 + kbt;
             const long long end = u1 < t1 ? u1 : t1;
             const bool whole = u == t0 && end == t1, starts = u == t0;
-            float v[kCols];
+            uint64_t v2[kSums / 2];  // pairs of rows
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
+            for (int i = 0; i < kSums / 2; ++i) v2[i] = 0;
             for (; u < end; ++u) {
                 // after a wait that ran out the loops go on without waiting, so
                 // that every barrier and ticket below is still met
-                if (ok) ok = __all_sync(0xffffffffu, wait_bounded_inline<false>(&tfull[buf], buf_phase, wctx));
+                if (ok) ok = __all_sync(0xffffffffu, wait_fast(&tfull[buf], buf_phase, wctx));
                 tc_fence_after();
-                const float4* s = reinterpret_cast<const float4*>(slots + slot * kCols);
-                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kCols);
-                if constexpr (kCols == 16) {
-                    uint32_t r[16];
-                    tmem_ld16(t, r);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+                const float* s = slots + slot * kCols + r0;
+                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kCols + r0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = s[i];
-                        fma2_rn(v[4 * i], v[4 * i + 1], __uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), f.x, f.y);
-                        fma2_rn(v[4 * i + 2], v[4 * i + 3], __uint_as_float(r[4 * i + 2]),
-                                __uint_as_float(r[4 * i + 3]), f.z, f.w);
-                    }
-                } else {
+                for (int a = 0; a < kA; ++a) {
+                    if constexpr (kRowsT == 16) {
+                        uint32_t r[16];
+                        tmem_ld16(t + a * kNT, r);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                                       "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                                       "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+                        const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(s + a * kNT);
 #pragma unroll
-                    for (int q = 0; q < kCols; q += 32) {
-                        uint32_t r[32];
-                        tmem_ld32(t + (uint32_t)q, r);
-                        tmem_wait_ld32(r);
+                        for (int i = 0; i < 4; ++i) {
+                            const ulonglong2 f = sa[i];
+                            fma_f32x2(v2[a * 8 + 2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
+                            fma_f32x2(v2[a * 8 + 2 * i + 1],
+                                      f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
+                        }
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 f = s[q / 4 + i];
-                            fma2_rn(v[q + 4 * i], v[q + 4 * i + 1], __uint_as_float(r[4 * i]),
-                                    __uint_as_float(r[4 * i + 1]), f.x, f.y);
-                            fma2_rn(v[q + 4 * i + 2], v[q + 4 * i + 3], __uint_as_float(r[4 * i + 2]),
-                                    __uint_as_float(r[4 * i + 3]), f.z, f.w);
+                        for (int c = 0; c < kRowsT; c += 32) {
+                            uint32_t r[32];
+                            tmem_ld32(t + (uint32_t)(a * kNT + c), r);
+                            tmem_wait_ld32(r);
+                            const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(s + a * kNT + c);
+                            uint64_t* vv = v2 + (a * kRowsT + c) / 2;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const ulonglong2 f = sa[i];
+                                fma_f32x2(vv[2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
+                                fma_f32x2(vv[2 * i + 1],
+                                          f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
+                            }
                         }
                     }
                 }
@@ -312,13 +326,16 @@ __global__ void __launch_bounds__(kFRThreads, 1)
             if (!whole) {
                 // this CTA's sums of the tile; slot 0 for a tile that began in an
                 // earlier share, slot 1 for one that begins here and goes on
-                const int rows = kMode == kRows ? min(kNT, p.M - (tile % p.MB) * kNT) : p.M;
-                float* part = p.parts + (size_t)(2 * c + (starts ? 1 : 0)) * (kCols * 128) + ch;
+                const int rows = (kMode == kRows ? min(kNT, p.M - (tile % p.MB) * kNT) : p.M) - r0;
+                float2* part = reinterpret_cast<float2*>(p.parts + (size_t)(2 * c + (starts ? 1 : 0)) * (kCols * 128)) +
+                               (size_t)(r0 / 2) * 128 + ch;  // rows in pairs: [kA][kNT / 2][128] of two
 #pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                    if (i % kNT < rows) __stcg(part + i * 128, v[i]);
+                for (int i = 0; i < kSums / 2; ++i) {
+                    const int a = i / (kRowsT / 2), j = i % (kRowsT / 2);
+                    if (2 * j < rows) __stcg(part + (size_t)(a * (kNT / 2) + j) * 128, f32x2_parts(v2[i]));
+                }
                 __threadfence();
-                named_bar_sync(1, 128);
+                named_bar_sync(1, kEpiThreads);
                 // the CTA that owns unit x is floor(((x + 1) C - 1) / units)
                 const int cf = (int)(((t0 + 1) * C - 1) / units), cl = (int)((t1 * C - 1) / units);
                 if (et == 0) {
@@ -327,19 +344,26 @@ __global__ void __launch_bounds__(kFRThreads, 1)
                     if (last) p.tickets[tile] = 0;  // ready for the next call
                     *last_flag = last;
                 }
-                named_bar_sync(1, 128);
+                named_bar_sync(1, kEpiThreads);
                 finish = *last_flag != 0;
                 if (finish) {
                     __threadfence();
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
+                    for (int i = 0; i < kSums / 2; ++i) v2[i] = 0;
                     for (int o = cf; o <= cl; ++o) {
                         // the first owner's share of the tile starts it, unless it starts mid-tile
                         const bool o_starts = o * units / C <= t0;
-                        const float* from = p.parts + (size_t)(2 * o + (o_starts ? 1 : 0)) * (kCols * 128) + ch;
+                        const float2* from =
+                            reinterpret_cast<const float2*>(p.parts + (size_t)(2 * o + (o_starts ? 1 : 0)) * (kCols * 128)) +
+                            (size_t)(r0 / 2) * 128 + ch;
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            if (i % kNT < rows) v[i] = __fadd_rn(v[i], __ldcg(from + i * 128));
+                        for (int i = 0; i < kSums / 2; ++i) {
+                            const int a = i / (kRowsT / 2), j = i % (kRowsT / 2);
+                            if (2 * j < rows) {
+                                const float2 x = __ldcg(from + (size_t)(a * (kNT / 2) + j) * 128), y = f32x2_parts(v2[i]);
+                                v2[i] = f32x2(__fadd_rn(y.x, x.x), __fadd_rn(y.y, x.y));
+                            }
+                        }
                     }
                 }
             }
@@ -347,13 +371,14 @@ __global__ void __launch_bounds__(kFRThreads, 1)
             if constexpr (kMode == kGateUp) {
                 const int a = tile / p.NB, nb = tile % p.NB, e = p.active[1 + a];
 #pragma unroll
-                for (int m = 0; m < kNT; ++m) {
-                    const float g = v[m];
-                    hbuf[m * 132 + ch] = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v[kNT + m]);
+                for (int i = 0; i < kRowsT / 2; ++i) {
+                    const float2 g = f32x2_parts(v2[i]), up = f32x2_parts(v2[kRowsT / 2 + i]);
+                    hbuf[(r0 + 2 * i) * 132 + ch] = __fmul_rn(__fdiv_rn(g.x, __fadd_rn(1.0f, expf(-g.x))), up.x);
+                    hbuf[(r0 + 2 * i + 1) * 132 + ch] = __fmul_rn(__fdiv_rn(g.y, __fadd_rn(1.0f, expf(-g.y))), up.y);
                 }
-                named_bar_sync(1, 128);
+                named_bar_sync(1, kEpiThreads);
 #pragma unroll 1
-                for (int it = et; it < kNT * 8; it += 128) {
+                for (int it = et; it < kNT * 8; it += kEpiThreads) {
                     const int m = it >> 3, col = (it & 7) * 16;
                     float f[16], amax = 0.0f;
 #pragma unroll
@@ -383,21 +408,24 @@ __global__ void __launch_bounds__(kFRThreads, 1)
                         if (col == 0) p.hs[((size_t)a * p.NB + nb) * p.M + m] = chosen ? s : 0.0f;
                     }
                 }
-                named_bar_sync(1, 128);  // hbuf has been read
+                named_bar_sync(1, kEpiThreads);  // hbuf has been read
             } else {
-                const int nb = kMode == kRows ? tile / p.MB : tile, m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
+                const int nb = kMode == kRows ? tile / p.MB : tile, m0 = (kMode == kRows ? (tile % p.MB) * kNT : 0) + r0;
                 const int n = nb * 128 + ch;
                 if (n < p.N) {
                     uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)m0 * p.N + n;
 #pragma unroll
-                    for (int m = 0; m < kNT; ++m)
-                        if (m0 + m < p.M) y[(size_t)m * p.N] = T::from_float(v[m]);
+                    for (int i = 0; i < kRowsT / 2; ++i) {
+                        const float2 f = f32x2_parts(v2[i]);
+                        if (m0 + 2 * i < p.M) y[(size_t)(2 * i) * p.N] = T::from_float(f.x);
+                        if (m0 + 2 * i + 1 < p.M) y[(size_t)(2 * i + 1) * p.N] = T::from_float(f.y);
+                    }
                 }
             }
         }
     } else {
         // ------------------------------------------------ scales, and codes with kFuse
-        const int sw = warp - 6;
+        const int sw = warp - 2;
         for (long long u = u0 + sw; u < u1; u += kFRSideWarps) {
             const long long i = u - u0;
             const int stage = (int)(i % kStages), slot = (int)(i % kSlots);
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kFRThreads, 1)
                     }
                 }
                 const float w = __ldg(p.ws + (size_t)tile * p.KB + kb);
-                ok = __all_sync(0xffffffffu, wait_bounded_inline<false>(&empty[stage], phase ^ 1, wctx));
+                ok = __all_sync(0xffffffffu, wait_fast(&empty[stage], phase ^ 1, wctx));
                 if (!ok) break;
                 uint8_t* sb = ring + stage * kStageBytes + kA * 16384;
 #pragma unroll
@@ -447,11 +475,11 @@ __global__ void __launch_bounds__(kFRThreads, 1)
                     if (kMode == kRows) {
                         const int row = (tile % p.MB) * kNT + m;
                         if (m < kNT && row < p.M)
-                            f[j] = __fmul_rn(p.xs[(size_t)kb * p.M + row], __ldg(p.ws + (size_t)(tile / p.MB) * p.KB + kb));
+                            f[j] = __fmul_rn(p.xs[kb * p.xs_pitch + row], __ldg(p.ws + (size_t)(tile / p.MB) * p.KB + kb));
                     } else if (kMode == kGateUp) {
                         const int e = p.active[1 + tile / p.NB], nb = tile % p.NB;
                         if (m < p.M) {
-                            const float xs = p.xs[(size_t)kb * p.M + m];
+                            const float xs = p.xs[kb * p.xs_pitch + m];
                             const size_t o = ((size_t)e * p.NB + nb) * p.KB + kb;
                             f[j] = __fmul_rn(xs, __ldg(p.ws + o));
                             g[j] = __fmul_rn(xs, __ldg(p.ws2 + o));
@@ -462,12 +490,12 @@ __global__ void __launch_bounds__(kFRThreads, 1)
                             float w = 0.0f;  // the token's weight for this expert
                             for (int q = 0; q < p.top_k; ++q)
                                 if (p.ids[m * p.top_k + q] == e) w = p.wts[m * p.top_k + q];
-                            f[j] = __fmul_rn(__fmul_rn(p.xs[((size_t)a * p.KB + ib) * p.M + m],
+                            f[j] = __fmul_rn(__fmul_rn(p.xs[((long long)a * p.KB + ib) * p.xs_pitch + m],
                                                        __ldg(p.ws + ((size_t)e * p.NB + tile) * p.KB + ib)), w);
                         }
                     }
                 }
-                ok = __all_sync(0xffffffffu, wait_bounded_inline<false>(&empty[stage], phase ^ 1, wctx));
+                ok = __all_sync(0xffffffffu, wait_fast(&empty[stage], phase ^ 1, wctx));
                 if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < (kNT + 31) / 32; ++j) {
