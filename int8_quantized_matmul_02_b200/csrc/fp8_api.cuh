@@ -9,8 +9,8 @@ constexpr int kMoeMaxTopK = 16;
 
 bool dtype_ok(int dtype) { return dtype == INT8MM_F16 || dtype == INT8MM_BF16; }
 
-// Columns of B of the weight-streaming kernel for M rows.
-int fp8_rows_nt(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+// Rows per tile of the weight-streaming kernel for M rows.
+int fp8_rows_nt(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 struct Fp8Layout {
     size_t codes, scales, total;
@@ -85,6 +85,7 @@ MoeWsLayout moe_ws_layout(int T, int H, int I, int E, int top_k) {
 }
 
 bool moe_shape_ok(int T, int H, int I, int E, int top_k) {
+    // (at most 256 experts of 2^20 units of 16 KB: units are counted in 32 bits)
     return T >= 1 && T <= kMoeMaxTokens && shape_ok(T, H, I) && I <= kMaxK && E >= 1 && E <= kMaxExperts &&
            top_k >= 1 && top_k <= kMoeMaxTopK && top_k <= E;
 }
@@ -152,7 +153,7 @@ cudaError_t launch_rows(int dev, int grid, const CUtensorMap& tw, const CUtensor
     static_assert(smem <= kMaxSmemOptin, "shared memory of one SM");
     cudaError_t e = fp8_opt_in<k_fp8_rows<kMode, kNT, kFuse, T>>(dev, smem);
     if (e != cudaSuccess) return e;
-    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kMode, kNT>()), smem, s, pdl, tw, tw2, tx, p);
+    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kNT>()), smem, s, pdl, tw, tw2, tx, p);
 }
 
 template <int kBN, typename T>
@@ -250,6 +251,10 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
     if (o.path != INT8MM_PATH_AUTO && o.path != INT8MM_PATH_GEMM && o.path != INT8MM_PATH_DECODE)
         return INT8MM_ERR_INVALID_ARGUMENT;
     if (o.path == INT8MM_PATH_DECODE && M > kFp8RowsMaxM) return INT8MM_ERR_INVALID_ARGUMENT;
+    // tiles and 16 KB units are counted in 32 bits (more of them than any GPU's memory holds)
+    if ((long long)cdiv(N, 128) * cdiv(M, 32) * cdiv(K, 128) > (INT32_MAX >> 4) && M <= kFp8RowsMaxM)
+        return INT8MM_ERR_INVALID_ARGUMENT;
+    if ((long long)cdiv(N, 128) * cdiv(M, kF8BM) > (INT32_MAX >> 1)) return INT8MM_ERR_INVALID_ARGUMENT;
     if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(ws, 256) || !aligned(w->codes, 16) || !aligned(w->scales, 4))
         return INT8MM_ERR_MISALIGNED;
     const Fp8WsLayout L = fp8_ws_layout(M, K, N);
@@ -266,7 +271,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
     const bool f16 = dtype == INT8MM_F16, timed = o.ev0 != nullptr;
     const bool rows = o.path == INT8MM_PATH_DECODE || (o.path == INT8MM_PATH_AUTO && fp8_rows_path(M, N, sms));
     const int nt = fp8_rows_nt(M);
-    const bool fuse = rows && nt <= 32;
+    const bool fuse = rows && nt == 32;
     cudaError_t e = cudaSuccess;
     if (!fuse) e = launch_quant_fp8(X, dtype, M, K, xq, xs, 1, fp8_pitch(M), info->sm_count, s);
     if (e != cudaSuccess) return cuda_status(e);
@@ -292,15 +297,14 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 128)) return INT8MM_ERR_CUDA;
         tb = ta;  // unused when the codes are made in the kernel
         if (!fuse && !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, (uint32_t)nt)) return INT8MM_ERR_CUDA;
-        const long long tiles = (long long)p.NB * p.MB;
-        const int grid = fr_shares(tiles * KB, tiles, sms);
+        const int grid = fr_shares(p.NB * p.MB * KB, p.NB * p.MB, sms);
         if (timed) e = cudaEventRecord(o.ev0, s);
         if (e != cudaSuccess) return cuda_status(e);
         const bool pdl = !timed;
 #define I8_ROWS(NT, FUSE)                                                                           \
     (f16 ? launch_rows<kRows, NT, FUSE, F16>(dev, grid, ta, ta, tb, p, s, pdl)                      \
          : launch_rows<kRows, NT, FUSE, BF16>(dev, grid, ta, ta, tb, p, s, pdl))
-        e = nt == 16 ? I8_ROWS(16, true) : nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
+        e = nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
 #undef I8_ROWS
     } else {
         constexpr int bn = 256;
@@ -315,7 +319,6 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         p.KB = KB;
         p.num_m_blocks = cdiv(M, kF8BM);
         p.num_n_blocks = cdiv(N, bn);
-        if ((long long)p.num_m_blocks * p.num_n_blocks > INT32_MAX / 2) return INT8MM_ERR_INVALID_ARGUMENT;
         p.num_tiles = p.num_m_blocks * p.num_n_blocks;
         // the largest group of row blocks whose codes fit in 48 MB of L2, at least 8
         const int fit = (int)std::min<uint64_t>(1u << 20, (48ull << 20) / ((uint64_t)kF8BM * (uint64_t)K));
@@ -426,10 +429,9 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     g.ws = w->gate_scales;
     g.ws2 = w->up_scales;
     g.tickets = reinterpret_cast<unsigned*>(b + L.t_gate);
-    const int ggrid = fr_shares((long long)A * IB * HB, (long long)A * IB, ctas);
-    e = nt == 16   ? launch_rows<kGateUp, 16, false, F16>(dev, ggrid, tg, tu, tx, g, s, true)
-        : nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, g, s, true)
-                   : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, g, s, true);
+    const int ggrid = fr_shares(A * IB * HB, A * IB, ctas);
+    e = nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, g, s, true)
+                 : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, g, s, true);
     if (e != cudaSuccess) return cuda_status(e);
     Fp8RowsParams d = p;
     d.N = H;
@@ -442,11 +444,11 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     d.Y = Y;
     d.test_flags = 0;
     d.tickets = reinterpret_cast<unsigned*>(b + L.t_down);
-    const int dgrid = fr_shares((long long)A * IB * HB, HB, ctas);
+    const int dgrid = fr_shares(A * IB * HB, HB, ctas);
 #define I8_DOWN(NT)                                                                        \
     (f16 ? launch_rows<kDown, NT, false, F16>(dev, dgrid, td, td, th, d, s, true)          \
          : launch_rows<kDown, NT, false, BF16>(dev, dgrid, td, td, th, d, s, true))
-    e = nt == 16 ? I8_DOWN(16) : nt == 32 ? I8_DOWN(32) : I8_DOWN(64);
+    e = nt == 32 ? I8_DOWN(32) : I8_DOWN(64);
 #undef I8_DOWN
     return cuda_status(e);
 }

@@ -4,19 +4,24 @@
 //
 //   out[m, n] = sum_b (xs[m, b] * ws[n / 128, b]) * sum_{k in block b} xq[m, k] * wq[n, k]
 //
-// Swapped operands: a 128-channel x 128-k box of the weight (16 KB, one 128 x
-// 128 scale block) is the A operand of tcgen05.mma (M = 128), the rows of X
-// are B (N = kNT >= rows).  A unit of work is one box (two in the gated
-// layer) with the rows' 128 k; its sums go to one of four TMEM accumulators,
-// and the epilogue thread of channel n (TMEM lane n) adds them, scaled, to one
-// running fp32 sum per row in registers.
+// A unit of work is one 128-channel x 128-k box of the weight (16 KB, one
+// scale block; two boxes in the gated layer) with the rows' 128 k.  The rows
+// are the A operand of tcgen05.mma (M = 128, of which only kNT rows are
+// staged: what the tensor core reads past them makes accumulator rows that
+// nobody reads), the channels are B (N = 128).  A unit's sums go to one of the
+// TMEM accumulators in rotation; the epilogue thread of row m (TMEM lane m)
+// adds them, times one scale, to running fp32 sums in registers.  (With the
+// operands the other way round a thread owns a channel and needs every row's
+// scale: the shared-memory reads of those, 16 bytes a time, slowed the tensor
+// core's own reads to 2400 cycles a unit for 128 rows, against 260.)
 //
 // The units, ordered by output tile and then k, are cut into equal consecutive
 // shares, one per CTA (one CTA per SM), whatever the shape: a CTA's share may
-// start and end inside a tile.  A tile that several CTAs share is finished by
-// the last of them to arrive (a ticket per tile): every one stores its fp32
-// sums, and the last adds them in the order of k, so the result does not
-// depend on who came last.  No CTA waits for another.
+// start and end inside a tile.  Of a tile that several CTAs share every one
+// stores its fp32 sums; at the end of its share, so that the stream is never
+// held up, each takes a ticket for its first and last tile, and the last one
+// to come adds the stored sums in the order of k: the result does not depend
+// on who that is, and no CTA waits for another.
 //
 // Three products are made of this:
 //   kRows    Y = X W;
@@ -27,17 +32,20 @@
 //            are one product over the concatenated k of the chosen experts,
 //            with the routing weight in the scale, so the weighted sum of a
 //            token's experts happens in the same running sums.
-// In the gated layer every token takes a column of B for every expert; tokens
-// that did not choose an expert have zero codes there.
+// In the gated layer every token is a row for every expert; tokens that did
+// not choose an expert have zero codes and scales there.
 //
-//   warp 0     TMA producer of the weight boxes (and of B unless kFuse);
-//   warp 1     TMEM allocation and MMA issue;
-//   warps 2-5  every fourth unit each: the unit's scale products into shared
-//              memory, and with kFuse the rows' codes (the rows' 16-bit values
-//              are read, quantised and written to the swizzled B operand);
-//   warps 6-   epilogue, TMEM lane quadrant w % 4: four warps, or eight with
-//              half of the rows each where a thread would have to hold more
-//              than 64 sums (128 of them spilled: 85 us for 100 x 11008 x 4096).
+// Warps: with rows in kQ of the four TMEM lane quadrants, the warps w with
+// w % 4 < kQ (w < 16) are the epilogue, one for each quadrant and quarter of
+// the channels (32 sums per thread and box: one load of 32 columns and 16
+// paired FMAs per unit, which keeps well below a unit's time); of the others
+//   the first   is the TMA producer of the weight boxes (and of the rows
+//               unless kFuse);
+//   the second  allocates TMEM and issues the MMAs;
+//   the rest    (up to ten) take the units in turn: the unit's scale products
+//               into shared memory, and with kFuse the rows' codes (the rows'
+//               16-bit values are read, quantised and written to the swizzled
+//               A operand).
 #pragma once
 
 #include "fp8_common.cuh"
@@ -66,94 +74,120 @@ struct Fp8RowsParams {
     void* Y;               // kRows, kDown: M x N, 16 bits
     uint8_t* hq;           // kGateUp: codes [a][M][N], scales [(a * NB + nb) * M + m]
     float* hs;
-    float* parts;          // two slots of kA x kNT x 128 floats per CTA
+    float* parts;          // two slots of kA x 128 x kNT floats per CTA
     unsigned* tickets;     // one per tile, zero between calls
     int* status;
     uint64_t wait_limit_ns;
     uint32_t test_flags;   // bit 0: block 0 never signals its first accumulator (timeout test)
 };
 
-constexpr int kFRBufs = 4;       // TMEM accumulators in rotation
-constexpr int kFRSideWarps = 4;
 constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
 constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
 
+// 16 epilogue warps leave no other below 16
+template <int kNT>
+__host__ __device__ constexpr int fr_threads() { return kNT == 128 ? 640 : 512; }
 template <int kMode>
 __host__ __device__ constexpr int fr_a() { return kMode == kGateUp ? 2 : 1; }
-template <int kMode, int kNT>
-__host__ __device__ constexpr int fr_epi_warps() { return fr_a<kMode>() * kNT > 64 ? 8 : 4; }
-template <int kMode, int kNT>
-__host__ __device__ constexpr int fr_threads() { return 32 * (2 + kFRSideWarps + fr_epi_warps<kMode, kNT>()); }
+template <int kMode>
+__host__ __device__ constexpr int fr_bufs() { return 512 / (128 * fr_a<kMode>()); }  // accumulators: all of TMEM
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stage_bytes() { return fr_a<kMode>() * 16384 + kNT * 128; }
 template <int kMode, int kNT>
-__host__ __device__ constexpr int fr_h_bytes() { return kMode == kGateUp ? kNT * 132 * 4 : 0; }
+__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + 4 * kNT * 4 + (fr_bufs<kMode>() + 1) * 8 + 64; }
+template <int kMode, int kNT>
+__host__ __device__ constexpr int fr_bytes(int stages) {
+    return fr_fixed_bytes<kMode, kNT>() + stages * (fr_stage_bytes<kMode, kNT>() + 16) +
+           (stages + fr_bufs<kMode>()) * fr_a<kMode>() * kNT * 4;
+}
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stages() {
     int s = 12;
-    while (1024 + s * (fr_stage_bytes<kMode, kNT>() + fr_a<kMode>() * kNT * 4 + 16) +
-               kFRBufs * (fr_a<kMode>() * kNT * 4 + 16) + fr_h_bytes<kMode, kNT>() + 256 > 232448)
-        --s;
+    while (fr_bytes<kMode, kNT>(s) > 232448) --s;
     return s;
 }
 template <int kMode, int kNT>
-__host__ __device__ constexpr int fr_smem_bytes() {
-    constexpr int s = fr_stages<kMode, kNT>();
-    return 1024 + s * fr_stage_bytes<kMode, kNT>() + (s + kFRBufs) * fr_a<kMode>() * kNT * 4 +
-           fr_h_bytes<kMode, kNT>() + (2 * s + 2 * kFRBufs + 1) * 8 + 64;
-}
+__host__ __device__ constexpr int fr_smem_bytes() { return fr_bytes<kMode, kNT>(fr_stages<kMode, kNT>()); }
 
 // Shares for `units` units in `tiles` tiles on at most `ctas` CTAs.
-__host__ __device__ __forceinline__ int fr_shares(long long units, long long tiles, int ctas) {
-    const long long want = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
-    return (int)(want < ctas ? want : ctas);
+__host__ __device__ __forceinline__ int fr_shares(int units, int tiles, int ctas) {
+    const int want = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
+    return want < ctas ? want : ctas;
+}
+
+// The shares: of `per` units each, the first `more` of them one unit more.
+// (Units are 16 KB of weight each, so their number is far below 2^31.)
+struct FrShares {
+    int per, more;
+    __device__ __forceinline__ int start(int share) const { return share * per + min(share, more); }
+    __device__ __forceinline__ int owner(int unit) const {
+        const int big = more * (per + 1);
+        return unit < big ? unit / (per + 1) : more + (unit - big) / per;
+    }
+};
+
+// silu(g) * u
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
+}
+
+// Nothing that follows is moved before the computation of v, nor that after it.
+__device__ __forceinline__ void pin16(uint64_t (&v)[16]) {
+    asm volatile("" : "+l"(v[0]), "+l"(v[1]), "+l"(v[2]), "+l"(v[3]), "+l"(v[4]), "+l"(v[5]), "+l"(v[6]), "+l"(v[7]),
+                 "+l"(v[8]), "+l"(v[9]), "+l"(v[10]), "+l"(v[11]), "+l"(v[12]), "+l"(v[13]), "+l"(v[14]),
+                 "+l"(v[15])::"memory");
 }
 
 template <int kMode, int kNT, bool kFuse, typename T>
-__global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
+__global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     k_fp8_rows(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_w2,
                const __grid_constant__ CUtensorMap tm_x, const Fp8RowsParams p) {
     constexpr int kA = fr_a<kMode>();
     constexpr int kStageBytes = fr_stage_bytes<kMode, kNT>();
     constexpr int kStages = fr_stages<kMode, kNT>();
-    constexpr int kSlots = kStages + kFRBufs;
-    constexpr int kCols = kA * kNT;  // columns of an accumulator
-    constexpr int kEpi = fr_epi_warps<kMode, kNT>(), kEpiThreads = 32 * kEpi;
-    constexpr int kRowsT = kNT / (kEpi / 4);  // rows per epilogue thread
-    constexpr int kSums = kA * kRowsT;        // running sums per epilogue thread
-    constexpr uint32_t kTmemCols = kFRBufs * kCols < 32 ? 32 : kFRBufs * kCols;
-    static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
+    constexpr int kBufs = fr_bufs<kMode>();
+    constexpr int kSlots = kStages + kBufs;
+    constexpr int kQ = kNT / 32;                   // TMEM lane quadrants with rows
+    constexpr int kEpiThreads = 4 * kQ * 32;
+    constexpr int kSpare = fr_threads<kNT>() / 32 - 4 * kQ - 2;  // warps that make scales (and codes):
+    constexpr int kSide = kFuse || kSpare < 4 ? kSpare : 4;      // all of those left over if there are codes to make
+    static_assert(kNT == 32 || kNT == 64 || kNT == 128, "rows");
+    // a stage's MMAs may complete again only after the epilogue has seen their last completion
+    static_assert(kStages > kBufs, "stages");
+    // a side warp waits for the stage's last completion by parity, so it must not be two rounds
+    // ahead: its previous unit, kSide earlier, has seen that unit's stage done one round earlier
+    static_assert(kSide <= kStages, "side warps");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring = smem;
+    uint8_t* xring = smem;                         // [stages][kNT rows]; M = 128 reads run on into wring
+    uint8_t* wring = smem + kStages * kNT * 128;   // [stages][kA boxes]
     // scale products of the units in flight.  A slot is rewritten kSlots units
     // later; its writer has seen the MMAs of kStages units earlier done, and
     // those were issued after the epilogue had read the slot's last content
     // (an accumulator is released only once its scales have been read).
-    float* slots = reinterpret_cast<float*>(ring + kStages * kStageBytes);
-    float* hbuf = slots + kSlots * kCols;  // kGateUp: [kNT][132]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(hbuf) + fr_h_bytes<kMode, kNT>());
-    uint64_t* full = bars;
-    uint64_t* empty = bars + kStages;
-    uint64_t* tfull = bars + 2 * kStages;
-    uint64_t* tempty = tfull + kFRBufs;
-    uint64_t* drain = tempty + kFRBufs;
+    float* slots = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // [slots][kA][kNT]
+    float* hmax = slots + kSlots * kA * kNT;       // kGateUp: [4][kNT]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(hmax + 4 * kNT);
+    uint64_t* full = bars;                         // [stages] boxes, rows and scales are there
+    uint64_t* done = bars + kStages;               // [stages] the stage's MMAs are complete
+    uint64_t* tempty = bars + 2 * kStages;         // [bufs] the epilogue has read the accumulator
+    uint64_t* drain = tempty + kBufs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* last_flag = abort_flag + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool epilogue = warp < 16 && (warp & 3) < kQ;
+    // the others, counted: 0 producer, 1 MMA issuer, 2 and on side warps
+    const int role = epilogue ? -1 : warp >= 16 ? warp - 16 : (warp >> 2) * (4 - kQ) + (warp & 3) - kQ;
     WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 2);  // the producer's expected bytes and the side warp
-            mbar_init(&empty[s], 1);
+            mbar_init(&done[s], 1);
         }
-        for (int b = 0; b < kFRBufs; ++b) {
-            mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kEpi);
-        }
+        for (int b = 0; b < kBufs; ++b) mbar_init(&tempty[b], 4 * kQ);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -161,8 +195,8 @@ __global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
         if (kMode == kGateUp) prefetch_tmap(&tm_w2);
         if (!kFuse) prefetch_tmap(&tm_x);
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, kTmemCols);
+    if (role == 1) {
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -177,37 +211,38 @@ __global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
 
     const int n_active = kMode == kRows ? 1 : p.active[0];
     const int kbt = kMode == kDown ? p.KB * n_active : p.KB;  // units per tile
-    const long long tiles = kMode == kRows ? (long long)p.NB * p.MB
-                            : kMode == kGateUp ? (long long)p.NB * n_active : (long long)p.NB;
-    const long long units = tiles * kbt;
+    const int tiles = kMode == kRows ? p.NB * p.MB : kMode == kGateUp ? p.NB * n_active : p.NB;
+    const int units = tiles * kbt;
     const int C = fr_shares(units, tiles, (int)gridDim.x);
     const int c = (int)blockIdx.x;
-    const long long u0 = c < C ? c * units / C : 0, u1 = c < C ? (c + 1) * units / C : 0;
+    const FrShares sh{units / C, units % C};
+    const int nu = c < C ? sh.start(c + 1) - sh.start(c) : 0;  // this CTA's units
+    const int first_tile = sh.start(c) / kbt, first_kb = sh.start(c) - first_tile * kbt;
 
-    if (warp == 0) {
+    if (role == 0) {
         // ------------------------------------------------ TMA producer
         if (elect_one()) {
             const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0;
-            int tile = (int)(u0 / kbt), kb = (int)(u0 - (long long)tile * kbt);
-            for (long long u = u0; u < u1; ++u) {
-                if (!wait_fast(&empty[stage], phase ^ 1, wctx)) break;
-                uint8_t* sa = ring + stage * kStageBytes;
-                uint8_t* sb = sa + kA * 16384;
+            int tile = first_tile, kb = first_kb;
+            for (int i = 0; i < nu; ++i) {
+                if (!wait_fast(&done[stage], phase ^ 1, wctx)) break;
+                uint8_t* sw = wring + stage * (kA * 16384);
+                uint8_t* sx = xring + stage * (kNT * 128);
                 mbar_arrive_expect_tx(&full[stage], kFuse ? kA * 16384 : kStageBytes);
                 if (kMode == kRows) {
-                    tma_load_2d(sa, &tm_w, &full[stage], kb * 128, (tile / p.MB) * 128, pol_w);
-                    if (!kFuse) tma_load_2d(sb, &tm_x, &full[stage], kb * 128, (tile % p.MB) * kNT, pol_x);
+                    tma_load_2d(sw, &tm_w, &full[stage], kb * 128, (tile / p.MB) * 128, pol_w);
+                    if (!kFuse) tma_load_2d(sx, &tm_x, &full[stage], kb * 128, (tile % p.MB) * kNT, pol_x);
                 } else if (kMode == kGateUp) {
                     const int e = p.active[1 + tile / p.NB], nb = tile % p.NB;
-                    tma_load_3d(sa, &tm_w, &full[stage], kb * 128, nb * 128, e, pol_w);
-                    tma_load_3d(sa + 16384, &tm_w2, &full[stage], kb * 128, nb * 128, e, pol_w);
-                    tma_load_2d(sb, &tm_x, &full[stage], kb * 128, 0, pol_x);
+                    tma_load_3d(sw, &tm_w, &full[stage], kb * 128, nb * 128, e, pol_w);
+                    tma_load_3d(sw + 16384, &tm_w2, &full[stage], kb * 128, nb * 128, e, pol_w);
+                    tma_load_2d(sx, &tm_x, &full[stage], kb * 128, 0, pol_x);
                 } else {
                     const int a = kb / p.KB, ib = kb - a * p.KB;
-                    tma_load_3d(sa, &tm_w, &full[stage], ib * 128, tile * 128, p.active[1 + a], pol_w);
-                    tma_load_3d(sb, &tm_x, &full[stage], ib * 128, 0, a, pol_x);
+                    tma_load_3d(sw, &tm_w, &full[stage], ib * 128, tile * 128, p.active[1 + a], pol_w);
+                    tma_load_3d(sx, &tm_x, &full[stage], ib * 128, 0, a, pol_x);
                 }
                 if (++stage == kStages) {
                     stage = 0;
@@ -219,31 +254,31 @@ __global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
                 }
             }
         }
-    } else if (warp == 1) {
+    } else if (role == 1) {
         // ------------------------------------------------ MMA issuer
         if (elect_one()) {
-            const uint32_t idesc = idesc_e4m3_f32(128, kNT);
+            const uint32_t idesc = idesc_e4m3_f32(128, 128);
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
-            bool issued = false;
-            for (long long u = u0; u < u1; ++u) {
-                if (!wait_fast(&tempty[buf], buf_phase ^ 1, wctx) || !wait_fast(&full[stage], phase, wctx))
-                    break;
+            bool issued = false, loaded = false;
+            for (int i = 0; i < nu; ++i) {
+                if (!wait_fast(&tempty[buf], buf_phase ^ 1, wctx)) break;
+                if (!loaded && !wait_fast(&full[stage], phase, wctx)) break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(ring + stage * kStageBytes);
-                const uint64_t db = sdesc_k128sw(sa + kA * 16384);
-                const uint32_t d = tmem_base + (uint32_t)(buf * kCols);
+                const uint64_t dx = sdesc_k128sw(smem_u32(xring + stage * (kNT * 128)));
+                const uint32_t sw = smem_u32(wring + stage * (kA * 16384));
+                const uint32_t d = tmem_base + (uint32_t)(buf * kA * 128);
 #pragma unroll
-                for (int i = 0; i < kA; ++i)
-                    mma_e4m3_k128(d + (uint32_t)(i * kNT), sdesc_k128sw(sa + i * 16384), db, idesc);
+                for (int a = 0; a < kA; ++a)
+                    mma_e4m3_k128(d + (uint32_t)(a * 128), dx, sdesc_k128sw(sw + a * 16384), idesc);
                 issued = true;
-                tc_commit(&empty[stage]);
-                if (!((p.test_flags & 1u) && c == 0 && u == u0)) tc_commit(&tfull[buf]);
+                if (!((p.test_flags & 1u) && c == 0 && i == 0)) tc_commit(&done[stage]);
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1;
                 }
-                if (++buf == kFRBufs) {
+                loaded = mbar_try_wait(&full[stage], phase);  // while this unit's MMAs run
+                if (++buf == kBufs) {
                     buf = 0;
                     buf_phase ^= 1;
                 }
@@ -253,229 +288,273 @@ __global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
                 wait_drain(drain, 0, kDrainLimitNs);
             }
         }
-    } else if (warp >= 2 + kFRSideWarps) {
+    } else if (epilogue) {
         // ------------------------------------------------ epilogue
-        const int quad = warp & 3, ch = quad * 32 + lane;
-        const int et = (int)threadIdx.x - 32 * (2 + kFRSideWarps);  // 0 .. kEpiThreads - 1
-        const int r0 = (et >> 7) * kRowsT;                           // this thread's first row
-        int buf = 0, slot = 0;
-        uint32_t buf_phase = 0;
+        const int quad = warp & 3, c0 = (warp >> 2) * 32;  // channels c0 .. c0 + 31 of the tile
+        const int row = quad * 32 + lane;
+        const bool lead = warp == 0 && lane == 0;
+        int buf = 0, slot = 0, stage = 0;
+        uint32_t phase = 0;
         bool ok = true;
-        long long u = u0;
-        while (u < u1) {
-            const int tile = (int)(u / kbt);
-            const long long t0 = (long long)tile * kbt, t1 = t0 + kbt;
-            const long long end = u1 < t1 ? u1 : t1;
-            const bool whole = u == t0 && end == t1, starts = u == t0;
-            uint64_t v2[kSums / 2];  // pairs of rows
+        int head_tile = -1, last_tile = -1;  // tiles shared with other CTAs, at the share's start and end
+        int tile = first_tile, kb = first_kb;
+        for (int left = nu; left > 0; ++tile, kb = 0) {
+            const int seg = min(kbt - kb, left);  // this share's units of the tile
+            const bool starts = kb == 0, whole = seg == kbt;
+            uint64_t v[kA][16];  // pairs of channels c0 + 2 i, + 1
 #pragma unroll
-            for (int i = 0; i < kSums / 2; ++i) v2[i] = 0;
-            for (; u < end; ++u) {
+            for (int a = 0; a < kA; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[a][i] = 0;
+            for (int i = 0; i < seg; ++i) {
+                float s1[kA];
                 // after a wait that ran out the loops go on without waiting, so
                 // that every barrier and ticket below is still met
-                if (ok) ok = __all_sync(0xffffffffu, wait_fast(&tfull[buf], buf_phase, wctx));
+                if (ok) ok = __all_sync(0xffffffffu, wait_fast(&done[stage], phase, wctx));
                 tc_fence_after();
-                const float* s = slots + slot * kCols + r0;
-                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kCols + r0);
+#pragma unroll
+                for (int a = 0; a < kA; ++a) s1[a] = slots[(slot * kA + a) * kNT + row];
+                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kA * 128 + c0);
 #pragma unroll
                 for (int a = 0; a < kA; ++a) {
-                    if constexpr (kRowsT == 16) {
-                        uint32_t r[16];
-                        tmem_ld16(t + a * kNT, r);
-                        asm volatile("tcgen05.wait::ld.sync.aligned;"
-                                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                                       "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                                       "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-                        const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(s + a * kNT);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const ulonglong2 f = sa[i];
-                            fma_f32x2(v2[a * 8 + 2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
-                            fma_f32x2(v2[a * 8 + 2 * i + 1],
-                                      f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kRowsT; c += 32) {
-                            uint32_t r[32];
-                            tmem_ld32(t + (uint32_t)(a * kNT + c), r);
-                            tmem_wait_ld32(r);
-                            const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(s + a * kNT + c);
-                            uint64_t* vv = v2 + (a * kRowsT + c) / 2;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const ulonglong2 f = sa[i];
-                                fma_f32x2(vv[2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
-                                fma_f32x2(vv[2 * i + 1],
-                                          f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
-                            }
-                        }
-                    }
+                    uint32_t r[32];
+                    tmem_ld32(t + (uint32_t)(a * 128), r);
+                    tmem_wait_ld32(r);
+                    fma32(v[a], r, f32x2(s1[a], s1[a]));
+                    if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tempty[buf]);
-                if (++buf == kFRBufs) {
-                    buf = 0;
-                    buf_phase ^= 1;
-                }
+                if (++buf == kBufs) buf = 0;
                 if (++slot == kSlots) slot = 0;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
+            left -= seg;
 
-            bool finish = true;
+            const int m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
+            const bool in = m0 + row < p.M;
             if (!whole) {
-                // this CTA's sums of the tile; slot 0 for a tile that began in an
-                // earlier share, slot 1 for one that begins here and goes on
-                const int rows = (kMode == kRows ? min(kNT, p.M - (tile % p.MB) * kNT) : p.M) - r0;
-                float2* part = reinterpret_cast<float2*>(p.parts + (size_t)(2 * c + (starts ? 1 : 0)) * (kCols * 128)) +
-                               (size_t)(r0 / 2) * 128 + ch;  // rows in pairs: [kA][kNT / 2][128] of two
+                // this CTA's sums of the tile, [kNT rows][kA][128 channels]; slot 0 for a
+                // tile that began in an earlier share, slot 1 for one that begins here
+                if (in) {
+                    float4* part = reinterpret_cast<float4*>(p.parts + (size_t)(2 * c + (starts ? 1 : 0)) * (kNT * kA * 128) +
+                                                             (size_t)row * (kA * 128) + c0);
 #pragma unroll
-                for (int i = 0; i < kSums / 2; ++i) {
-                    const int a = i / (kRowsT / 2), j = i % (kRowsT / 2);
-                    if (2 * j < rows) __stcg(part + (size_t)(a * (kNT / 2) + j) * 128, f32x2_parts(v2[i]));
+                    for (int a = 0; a < kA; ++a)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 x = f32x2_parts(v[a][2 * i]), y = f32x2_parts(v[a][2 * i + 1]);
+                            __stcg(part + a * 32 + i, make_float4(x.x, x.y, y.x, y.y));
+                        }
                 }
-                __threadfence();
-                named_bar_sync(1, kEpiThreads);
-                // the CTA that owns unit x is floor(((x + 1) C - 1) / units)
-                const int cf = (int)(((t0 + 1) * C - 1) / units), cl = (int)((t1 * C - 1) / units);
-                if (et == 0) {
-                    const unsigned old = atomicAdd(&p.tickets[tile], 1u);
-                    const bool last = old == (unsigned)(cl - cf);
-                    if (last) p.tickets[tile] = 0;  // ready for the next call
-                    *last_flag = last;
+                if (starts)
+                    last_tile = tile;
+                else
+                    head_tile = tile;
+                continue;
+            }
+            if constexpr (kMode == kGateUp) {
+                const int a = tile / p.NB, nb = tile % p.NB, e = p.active[1 + a];
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 g = f32x2_parts(v[0][i]), up = f32x2_parts(v[kA - 1][i]);
+                    const float hx = silu_mul(g.x, up.x), hy = silu_mul(g.y, up.y);
+                    amax = fmaxf(amax, fmaxf(fabsf(hx), fabsf(hy)));
+                    v[0][i] = f32x2(hx, hy);
+                    asm volatile("" : "+l"(v[0][i])::"memory");  // one pair at a time, in few registers
                 }
+                hmax[(c0 / 32) * kNT + row] = amax;
                 named_bar_sync(1, kEpiThreads);
-                finish = *last_flag != 0;
-                if (finish) {
-                    __threadfence();
+                amax = fmaxf(fmaxf(hmax[row], hmax[kNT + row]), fmaxf(hmax[2 * kNT + row], hmax[3 * kNT + row]));
+                if (in) {
+                    bool chosen = false;
+                    for (int j = 0; j < p.top_k; ++j) chosen |= p.ids[row * p.top_k + j] == e;
+                    const float s = fp8_block_scale(amax), inv = __frcp_rn(s);
+                    uint8_t* dst = p.hq + ((size_t)a * p.M + row) * p.N + nb * 128 + c0;
 #pragma unroll
-                    for (int i = 0; i < kSums / 2; ++i) v2[i] = 0;
-                    for (int o = cf; o <= cl; ++o) {
-                        // the first owner's share of the tile starts it, unless it starts mid-tile
-                        const bool o_starts = o * units / C <= t0;
-                        const float2* from =
-                            reinterpret_cast<const float2*>(p.parts + (size_t)(2 * o + (o_starts ? 1 : 0)) * (kCols * 128)) +
-                            (size_t)(r0 / 2) * 128 + ch;
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < kSums / 2; ++i) {
-                            const int a = i / (kRowsT / 2), j = i % (kRowsT / 2);
-                            if (2 * j < rows) {
-                                const float2 x = __ldcg(from + (size_t)(a * (kNT / 2) + j) * 128), y = f32x2_parts(v2[i]);
-                                v2[i] = f32x2(__fadd_rn(y.x, x.x), __fadd_rn(y.y, x.y));
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 x = f32x2_parts(v[0][8 * q + 2 * i]), y = f32x2_parts(v[0][8 * q + 2 * i + 1]);
+                            w[i] = chosen ? e4m3x4(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(y.x, inv),
+                                                   __fmul_rn(y.y, inv))
+                                          : 0u;
+                        }
+                        if (nb * 128 + c0 + q * 16 < p.N)  // N % 16 == 0
+                            *reinterpret_cast<uint4*>(dst + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (c0 == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? s : 0.0f;
+                }
+                named_bar_sync(1, kEpiThreads);  // hmax has been read
+            } else {
+                const int n = (kMode == kRows ? tile / p.MB : tile) * 128 + c0;
+                if (in) {
+                    uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = f32x2_parts(v[0][4 * q + i]);
+                            w[i] = T::pack(f.x, f.y);
+                        }
+                        if (n + q * 8 < p.N)  // N % 16 == 0
+                            *reinterpret_cast<uint4*>(y + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+        // The shared tiles come last, after the share has been streamed: their
+        // sums are stored by now, and nothing waits for what follows.
+        if (head_tile >= 0 || last_tile >= 0) {
+            __threadfence();
+            named_bar_sync(1, kEpiThreads);
+            if (lead) {
+                int f = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = i == 0 ? head_tile : last_tile;
+                    if (t < 0) continue;
+                    const int others = sh.owner((t + 1) * kbt - 1) - sh.owner(t * kbt);
+                    if (atomicAdd(&p.tickets[t], 1u) == (unsigned)others) {
+                        p.tickets[t] = 0;  // ready for the next call
+                        f |= 1 << i;
+                    }
+                }
+                *last_flag = f;
+            }
+            named_bar_sync(1, kEpiThreads);
+            const int f = *last_flag;
+            if (f) __threadfence();
+            const int ew = (warp >> 2) * kQ + (warp & 3);  // 0 .. 4 kQ - 1: a warp per row, 4 channels per lane
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                if (!((f >> i) & 1)) continue;
+                const int t = i == 0 ? head_tile : last_tile;
+                const int cf = sh.owner(t * kbt), cl = sh.owner((t + 1) * kbt - 1);
+                const int m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
+                const int nb = kMode == kRows ? t / p.MB : kMode == kGateUp ? t % p.NB : t;
+                const int n = nb * 128 + 4 * lane;
+                constexpr int kR = 4;  // rows whose loads are in flight together
+#pragma unroll 1
+                for (int r0 = ew; r0 < rows; r0 += 4 * kQ * kR) {
+                    float4 sum[kR][kA];
+#pragma unroll
+                    for (int r = 0; r < kR; ++r)
+#pragma unroll
+                        for (int a = 0; a < kA; ++a) sum[r][a] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int o = cf; o <= cl; ++o) {  // in the order of k
+                        const float4* from =
+                            reinterpret_cast<const float4*>(p.parts + (size_t)(2 * o + (sh.start(o) <= t * kbt ? 1 : 0)) *
+                                                                          (kNT * kA * 128)) + lane;
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            const int row = r0 + r * 4 * kQ;
+                            if (row < rows) {
+#pragma unroll
+                                for (int a = 0; a < kA; ++a) {
+                                    const float4 x = __ldcg(from + (row * kA + a) * 32);
+                                    sum[r][a].x = __fadd_rn(sum[r][a].x, x.x);
+                                    sum[r][a].y = __fadd_rn(sum[r][a].y, x.y);
+                                    sum[r][a].z = __fadd_rn(sum[r][a].z, x.z);
+                                    sum[r][a].w = __fadd_rn(sum[r][a].w, x.w);
+                                }
                             }
                         }
                     }
-                }
-            }
-            if (!finish) continue;
-            if constexpr (kMode == kGateUp) {
-                const int a = tile / p.NB, nb = tile % p.NB, e = p.active[1 + a];
 #pragma unroll
-                for (int i = 0; i < kRowsT / 2; ++i) {
-                    const float2 g = f32x2_parts(v2[i]), up = f32x2_parts(v2[kRowsT / 2 + i]);
-                    hbuf[(r0 + 2 * i) * 132 + ch] = __fmul_rn(__fdiv_rn(g.x, __fadd_rn(1.0f, expf(-g.x))), up.x);
-                    hbuf[(r0 + 2 * i + 1) * 132 + ch] = __fmul_rn(__fdiv_rn(g.y, __fadd_rn(1.0f, expf(-g.y))), up.y);
-                }
-                named_bar_sync(1, kEpiThreads);
-#pragma unroll 1
-                for (int it = et; it < kNT * 8; it += kEpiThreads) {
-                    const int m = it >> 3, col = (it & 7) * 16;
-                    float f[16], amax = 0.0f;
+                    for (int r = 0; r < kR; ++r) {
+                        const int row = r0 + r * 4 * kQ;
+                        if (row >= rows) continue;  // the same for the whole warp
+                        if constexpr (kMode == kGateUp) {
+                            const int a = t / p.NB, e = p.active[1 + a];
+                            const float4 g = sum[r][0], up = sum[r][kA - 1];
+                            const float4 h = make_float4(silu_mul(g.x, up.x), silu_mul(g.y, up.y), silu_mul(g.z, up.z),
+                                                         silu_mul(g.w, up.w));
+                            float amax = fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)));
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 h = *reinterpret_cast<const float4*>(hbuf + m * 132 + col + i);
-                        f[i] = h.x, f[i + 1] = h.y, f[i + 2] = h.z, f[i + 3] = h.w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-#pragma unroll
-                    for (int d = 4; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-                    if (m < p.M) {
-                        bool chosen = false;
-                        for (int j = 0; j < p.top_k; ++j) chosen |= p.ids[m * p.top_k + j] == e;
-                        const float s = fp8_block_scale(amax), inv = __frcp_rn(s);
-                        uint4 q = make_uint4(0, 0, 0, 0);
-                        if (chosen) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = e4m3x4(__fmul_rn(f[4 * i], inv), __fmul_rn(f[4 * i + 1], inv),
-                                              __fmul_rn(f[4 * i + 2], inv), __fmul_rn(f[4 * i + 3], inv));
-                            q = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                            const bool chosen = __any_sync(0xffffffffu, lane < p.top_k && p.ids[row * p.top_k + lane] == e);
+                            const float s = fp8_block_scale(amax), inv = __frcp_rn(s);
+                            const uint32_t q = chosen ? e4m3x4(__fmul_rn(h.x, inv), __fmul_rn(h.y, inv),
+                                                               __fmul_rn(h.z, inv), __fmul_rn(h.w, inv))
+                                                      : 0u;
+                            if (n < p.N) *reinterpret_cast<uint32_t*>(p.hq + ((size_t)a * p.M + row) * p.N + n) = q;
+                            if (lane == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? s : 0.0f;
+                        } else if (n < p.N) {  // N % 16 == 0
+                            const float4 x = sum[r][0];
+                            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n) =
+                                make_uint2(T::pack(x.x, x.y), T::pack(x.z, x.w));
                         }
-                        if (nb * 128 + col < p.N)  // N % 16 == 0
-                            *reinterpret_cast<uint4*>(p.hq + ((size_t)a * p.M + m) * p.N + nb * 128 + col) = q;
-                        if (col == 0) p.hs[((size_t)a * p.NB + nb) * p.M + m] = chosen ? s : 0.0f;
-                    }
-                }
-                named_bar_sync(1, kEpiThreads);  // hbuf has been read
-            } else {
-                const int nb = kMode == kRows ? tile / p.MB : tile, m0 = (kMode == kRows ? (tile % p.MB) * kNT : 0) + r0;
-                const int n = nb * 128 + ch;
-                if (n < p.N) {
-                    uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)m0 * p.N + n;
-#pragma unroll
-                    for (int i = 0; i < kRowsT / 2; ++i) {
-                        const float2 f = f32x2_parts(v2[i]);
-                        if (m0 + 2 * i < p.M) y[(size_t)(2 * i) * p.N] = T::from_float(f.x);
-                        if (m0 + 2 * i + 1 < p.M) y[(size_t)(2 * i + 1) * p.N] = T::from_float(f.y);
                     }
                 }
             }
         }
     } else {
         // ------------------------------------------------ scales, and codes with kFuse
-        const int sw = warp - 2;
-        for (long long u = u0 + sw; u < u1; u += kFRSideWarps) {
-            const long long i = u - u0;
-            const int stage = (int)(i % kStages), slot = (int)(i % kSlots);
+        const int sidx = role - 2;
+        int tile = first_tile, kb = first_kb + sidx;
+        while (kb >= kbt) {
+            kb -= kbt;
+            ++tile;
+        }
+        for (int i = sidx < kSide ? sidx : nu; i < nu; i += kSide) {
+            const int stage = i % kStages, slot = i % kSlots;
             const uint32_t phase = (uint32_t)(i / kStages) & 1u;
-            const int tile = (int)(u / kbt), kb = (int)(u - (long long)tile * kbt);
-            float* s = slots + slot * kCols;
-            bool ok;
+            float* s = slots + slot * (kA * kNT);
             if constexpr (kFuse) {
+                static_assert(kMode == kRows && kNT == 32, "fused codes: the plain product of at most 32 rows");
                 // 8 lanes per row, 16 values each; 4 rows per step
-                static_assert(!kFuse || kMode == kRows, "fused codes: plain product only");
                 const int chunk = lane & 7, rsub = lane >> 3;
                 const int k = kb * 128 + chunk * 16;
-                uint4 x[kNT / 4][2];
+                const int steps = (p.M + 3) >> 2;
+                uint4 x[8][2];
 #pragma unroll
-                for (int r = 0; r < kNT / 4; ++r) {
-                    const int m = r * 4 + rsub;
-                    x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
-                    if (m < p.M && k < p.K) {  // K % 16 == 0: all 16 values or none
-                        const uint4* src = reinterpret_cast<const uint4*>(p.X + (size_t)m * p.K + k);
-                        x[r][0] = __ldg(src);
-                        x[r][1] = __ldg(src + 1);
+                for (int r = 0; r < 8; ++r) {
+                    if (r < steps) {
+                        const int m = r * 4 + rsub;
+                        x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
+                        if (m < p.M && k < p.K) {  // K % 16 == 0: all 16 values or none
+                            const uint4* src = reinterpret_cast<const uint4*>(p.X + (size_t)m * p.K + k);
+                            x[r][0] = __ldg(src);
+                            x[r][1] = __ldg(src + 1);
+                        }
                     }
                 }
                 const float w = __ldg(p.ws + (size_t)tile * p.KB + kb);
-                ok = __all_sync(0xffffffffu, wait_fast(&empty[stage], phase ^ 1, wctx));
-                if (!ok) break;
-                uint8_t* sb = ring + stage * kStageBytes + kA * 16384;
+                if (!__all_sync(0xffffffffu, wait_fast(&done[stage], phase ^ 1, wctx))) break;
+                uint8_t* sx = xring + stage * (kNT * 128);
 #pragma unroll
-                for (int r = 0; r < kNT / 4; ++r) {
-                    const int m = r * 4 + rsub;
-                    float a = T::pair_max(fp8_amax8<T>(fp8_amax8<T>(T::as_pair(0u), x[r][0]), x[r][1]));
+                for (int r = 0; r < 8; ++r) {
+                    if (r < steps) {
+                        const int m = r * 4 + rsub;
+                        float a = T::pair_max(fp8_amax8<T>(fp8_amax8<T>(T::as_pair(0u), x[r][0]), x[r][1]));
 #pragma unroll
-                    for (int d = 4; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                    const float sc = fp8_block_scale(a), inv = __frcp_rn(sc);
-                    const uint2 lo = fp8_codes8<T>(x[r][0], inv), hi = fp8_codes8<T>(x[r][1], inv);
-                    *reinterpret_cast<uint4*>(sb + m * 128 + ((chunk ^ (m & 7)) << 4)) =
-                        make_uint4(lo.x, lo.y, hi.x, hi.y);
-                    if (chunk == 0) s[m] = __fmul_rn(sc, w);
+                        for (int d = 4; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+                        const float sc = fp8_block_scale(a), inv = __frcp_rn(sc);
+                        const uint2 lo = fp8_codes8<T>(x[r][0], inv), hi = fp8_codes8<T>(x[r][1], inv);
+                        *reinterpret_cast<uint4*>(sx + m * 128 + ((chunk ^ (m & 7)) << 4)) =
+                            make_uint4(lo.x, lo.y, hi.x, hi.y);
+                        if (chunk == 0) s[m] = __fmul_rn(sc, w);
+                    }
                 }
                 fence_proxy_async_smem();
             } else {
-                float f[(kNT + 31) / 32], g[(kNT + 31) / 32];
+                float f[kQ], g[kQ];
 #pragma unroll
-                for (int j = 0; j < (kNT + 31) / 32; ++j) {
+                for (int j = 0; j < kQ; ++j) {
                     const int m = lane + 32 * j;
                     f[j] = g[j] = 0.0f;
                     if (kMode == kRows) {
-                        const int row = (tile % p.MB) * kNT + m;
-                        if (m < kNT && row < p.M)
-                            f[j] = __fmul_rn(p.xs[kb * p.xs_pitch + row], __ldg(p.ws + (size_t)(tile / p.MB) * p.KB + kb));
+                        const int r = (tile % p.MB) * kNT + m;
+                        if (r < p.M)
+                            f[j] = __fmul_rn(p.xs[kb * p.xs_pitch + r], __ldg(p.ws + (size_t)(tile / p.MB) * p.KB + kb));
                     } else if (kMode == kGateUp) {
                         const int e = p.active[1 + tile / p.NB], nb = tile % p.NB;
                         if (m < p.M) {
@@ -495,28 +574,29 @@ __global__ void __launch_bounds__(fr_threads<kMode, kNT>(), 1)
                         }
                     }
                 }
-                ok = __all_sync(0xffffffffu, wait_fast(&empty[stage], phase ^ 1, wctx));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, wait_fast(&done[stage], phase ^ 1, wctx))) break;
 #pragma unroll
-                for (int j = 0; j < (kNT + 31) / 32; ++j) {
-                    const int m = lane + 32 * j;
-                    if (m < kNT) {
-                        s[m] = f[j];
-                        if (kA == 2) s[kNT + m] = g[j];
-                    }
+                for (int j = 0; j < kQ; ++j) {
+                    s[lane + 32 * j] = f[j];
+                    if (kA == 2) s[kNT + lane + 32 * j] = g[j];
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[stage]);
+            kb += kSide;
+            while (kb >= kbt) {
+                kb -= kbt;
+                ++tile;
+            }
         }
     }
 
     if (threadIdx.x == 0 && *abort_flag) settle_after_abort();  // copies issued before the abort land first
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (role == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc(tmem_base, 512);
     }
 }
 
