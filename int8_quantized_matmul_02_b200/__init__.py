@@ -396,6 +396,7 @@ _DTYPES = {torch.float16: _abi.F16, torch.bfloat16: _abi.BF16}
 
 
 _NO_SWITCH = contextlib.nullcontext()
+_current_stream = torch._C._cuda_getCurrentRawStream  # of a device, as the integer that the C interface takes
 
 
 def _on(device: torch.device, stream=None):
@@ -427,15 +428,20 @@ def quantize_fp8(X: torch.Tensor, codes: torch.Tensor | None = None, scales: tor
     value is code * scale."""
     if not (X.is_cuda and X.dtype in _DTYPES and X.dim() == 2 and X.is_contiguous()):
         raise ValueError("X must be a contiguous 2-D float16 or bfloat16 CUDA tensor")
+    dev = X.device
     M, K = X.shape
     kb = (K + 127) // 128
-    _check_out(codes, "codes", (M, K), torch.float8_e4m3fn, X.device)
-    _check_out(scales, "scales", (M, kb), torch.float32, X.device)
-    with _on(X.device, stream):
-        codes = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=X.device) if codes is None else codes
-        scales = torch.empty(M, kb, dtype=torch.float32, device=X.device) if scales is None else scales
-        _abi.check(_abi.load().int8mm_quantize_fp8(X.data_ptr(), _DTYPES[X.dtype], M, K, codes.data_ptr(),
-                                                   scales.data_ptr(), _stream(stream)), "int8mm_quantize_fp8")
+    _check_out(codes, "codes", (M, K), torch.float8_e4m3fn, dev)
+    _check_out(scales, "scales", (M, kb), torch.float32, dev)
+    with _on(dev, stream):
+        if codes is None:
+            codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        if scales is None:
+            scales = torch.empty((M, kb), dtype=torch.float32, device=dev)
+        st = _abi.load().int8mm_quantize_fp8(X.data_ptr(), _DTYPES[X.dtype], M, K, codes.data_ptr(), scales.data_ptr(),
+                                             _current_stream(dev.index))
+    if st:
+        _abi.check(st, "int8mm_quantize_fp8")
     return codes, scales
 
 
@@ -446,6 +452,7 @@ class Fp8Weight:
         self.codes = codes      # N x K float8_e4m3fn
         self.scales = scales    # ceil(N/128) x ceil(K/128) float32
         self.N, self.K = codes.shape
+        self.device = codes.device
         self.struct = _abi.Fp8Weight(self.K, self.N, codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.byref(self.struct)
 
@@ -486,7 +493,8 @@ def prepare_weight_fp8(W: torch.Tensor, stream=None) -> Fp8Weight:
     with _on(W.device, stream):
         buf = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
         _abi.check(lib.int8mm_prepare_weight_fp8(W.data_ptr(), _DTYPES[W.dtype], K, N, buf.data_ptr(), nbytes,
-                                                 ctypes.byref(st), _stream(stream)), "int8mm_prepare_weight_fp8")
+                                                 ctypes.byref(st), _current_stream(W.device.index)),
+                   "int8mm_prepare_weight_fp8")
     nb, kb = (N + 127) // 128, (K + 127) // 128
     return Fp8Weight(_view(buf, st.codes, N * K, torch.float8_e4m3fn, (N, K)),
                      _view(buf, st.scales, nb * kb, torch.float32, (nb, kb)))
@@ -519,7 +527,7 @@ def forward_fp8(X: torch.Tensor, w: Fp8Weight, *, out: torch.Tensor | None = Non
     quantised to e4m3 per row and block of 128 by the call, and the
     block-scaled weight; fp32 sums, Y in X's type.  path: "auto", "gemm"
     (tiled) or "decode" (weight-streaming, M <= 1024)."""
-    dev = w.codes.device
+    dev = w.device
     if X.dtype not in _DTYPES or X.dim() != 2 or X.shape[1] != w.K or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous float16 or bfloat16 tensor of shape (M, {w.K}) on {dev}")
     M = X.shape[0]
@@ -530,11 +538,12 @@ def forward_fp8(X: torch.Tensor, w: Fp8Weight, *, out: torch.Tensor | None = Non
     with _on(dev, stream):
         if workspace is None:
             workspace = Fp8Workspace(M, w.K, w.N, device=dev)
-        Y = out if out is not None else torch.empty(M, w.N, dtype=X.dtype, device=dev)
-        _abi.check(_abi.load().int8mm_forward_fp8(X.data_ptr(), _DTYPES[X.dtype], M, w.ref, Y.data_ptr(),
-                                                  workspace.buf.data_ptr(), workspace.nbytes,
-                                                  _fp8_opts(path, wait_limit_ns, test_flags), _stream(stream)),
-                   "int8mm_forward_fp8")
+        Y = out if out is not None else X.new_empty(M, w.N)
+        st = _abi.load().int8mm_forward_fp8(X.data_ptr(), _DTYPES[X.dtype], M, w.ref, Y.data_ptr(),
+                                            workspace.buf.data_ptr(), workspace.nbytes,
+                                            _fp8_opts(path, wait_limit_ns, test_flags), _current_stream(dev.index))
+    if st:
+        _abi.check(st, "int8mm_forward_fp8")
     return Y
 
 
@@ -547,6 +556,7 @@ class MoeFp8Weight:
     def __init__(self, router: torch.Tensor, gate, up, down):
         self.router, self.gate, self.up, self.down = router, gate, up, down
         self.E, self.I, self.H = gate[0].shape
+        self.device = router.device
         self.struct = _abi.MoeWeight(self.E, self.H, self.I, router.data_ptr(),
                                      *(t.data_ptr() for pair in (gate, up, down) for t in pair))
         self.ref = ctypes.byref(self.struct)
@@ -611,7 +621,7 @@ def forward_moe_fp8(X: torch.Tensor, w: MoeFp8Weight, top_k: int, *, renormalize
     weights (renormalize: divided by their sum).  Returns Y, T x H in X's type,
     and with return_routing also the experts (int32 T x top_k, best first) and
     their weights (float32 T x top_k)."""
-    dev = w.router.device
+    dev = w.device
     if X.dtype != w.router.dtype or X.dim() != 2 or X.shape[1] != w.H or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous {w.router.dtype} tensor of shape (T, {w.H}) on {dev}")
     T = X.shape[0]
@@ -624,13 +634,15 @@ def forward_moe_fp8(X: torch.Tensor, w: MoeFp8Weight, top_k: int, *, renormalize
     with _on(dev, stream):
         if workspace is None:
             workspace = MoeWorkspace(T, w, top_k)
-        Y = out if out is not None else torch.empty(T, w.H, dtype=X.dtype, device=dev)
+        Y = out if out is not None else X.new_empty(T, w.H)
         if return_routing:
-            ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
-            wts = torch.empty(T, top_k, dtype=torch.float32, device=dev)
-        _abi.check(_abi.load().int8mm_forward_moe_fp8(
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+            wts = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        st = _abi.load().int8mm_forward_moe_fp8(
             X.data_ptr(), _DTYPES[X.dtype], T, w.ref, top_k, int(bool(renormalize)), Y.data_ptr(),
             ids.data_ptr() if return_routing else None, wts.data_ptr() if return_routing else None,
             workspace.buf.data_ptr(), workspace.nbytes, _fp8_opts("auto", wait_limit_ns, test_flags),
-            _stream(stream)), "int8mm_forward_moe_fp8")
+            _current_stream(dev.index))
+    if st:
+        _abi.check(st, "int8mm_forward_moe_fp8")
     return (Y, ids, wts) if return_routing else Y

@@ -45,7 +45,7 @@ Fp8WsLayout fp8_ws_layout(int M, int K, int N) {
         const int nt = fp8_rows_nt(M);
         o = align_up(o + (size_t)cdiv(N, 128) * cdiv(M, nt) * 4, 256);
         L.parts = o;
-        o = align_up(o + (size_t)2 * kFRMaxCtas * nt * 128 * 4, 256);
+        o = align_up(o + (size_t)2 * kFRMaxCtas * std::min(M, nt) * 128 * 4, 256);
     }
     L.total = o;
     return L;
@@ -79,7 +79,7 @@ MoeWsLayout moe_ws_layout(int T, int H, int I, int E, int top_k) {
     L.xs = take((size_t)T * cdiv(H, 128) * 4);
     L.hq = take((size_t)A * T * I);
     L.hs = take((size_t)A * T * cdiv(I, 128) * 4);
-    L.parts = take((size_t)2 * kFRMaxCtas * 2 * fp8_rows_nt(T) * 128 * 4);
+    L.parts = take((size_t)4 * kFRMaxCtas * T * 2 * 128 * 4);
     L.total = o;
     return L;
 }
@@ -148,12 +148,13 @@ cudaError_t launch_quant_fp8(const uint16_t* X, int dtype, int M, int K, uint8_t
 
 template <int kMode, int kNT, bool kFuse, typename T>
 cudaError_t launch_rows(int dev, int grid, const CUtensorMap& tw, const CUtensorMap& tw2, const CUtensorMap& tx,
-                        const Fp8RowsParams& p, cudaStream_t s, bool pdl) {
+                        const CUtensorMap& tnext, const Fp8RowsParams& p, cudaStream_t s, bool pdl) {
     constexpr int smem = fr_smem_bytes<kMode, kNT>();
     static_assert(smem <= kMaxSmemOptin, "shared memory of one SM");
     cudaError_t e = fp8_opt_in<k_fp8_rows<kMode, kNT, kFuse, T>>(dev, smem);
     if (e != cudaSuccess) return e;
-    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kNT>()), smem, s, pdl, tw, tw2, tx, p);
+    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kNT>()), smem, s, pdl, tw, tw2, tx,
+                  tnext, p);
 }
 
 template <int kBN, typename T>
@@ -290,6 +291,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         p.ws = w->scales;
         p.Y = Y;
         p.parts = reinterpret_cast<float*>(b + L.parts);
+        p.part_rows = std::min(M, nt);
         p.tickets = reinterpret_cast<unsigned*>(b + L.tickets);
         p.status = reinterpret_cast<int*>(b + L.status);
         p.wait_limit_ns = o.wait_ns;
@@ -297,13 +299,13 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 128)) return INT8MM_ERR_CUDA;
         tb = ta;  // unused when the codes are made in the kernel
         if (!fuse && !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, (uint32_t)nt)) return INT8MM_ERR_CUDA;
-        const int grid = fr_shares(p.NB * p.MB * KB, p.NB * p.MB, sms);
+        const int grid = FrShares(p.NB * p.MB, KB, sms).count;
         if (timed) e = cudaEventRecord(o.ev0, s);
         if (e != cudaSuccess) return cuda_status(e);
         const bool pdl = !timed;
 #define I8_ROWS(NT, FUSE)                                                                           \
-    (f16 ? launch_rows<kRows, NT, FUSE, F16>(dev, grid, ta, ta, tb, p, s, pdl)                      \
-         : launch_rows<kRows, NT, FUSE, BF16>(dev, grid, ta, ta, tb, p, s, pdl))
+    (f16 ? launch_rows<kRows, NT, FUSE, F16>(dev, grid, ta, ta, tb, ta, p, s, pdl)                  \
+         : launch_rows<kRows, NT, FUSE, BF16>(dev, grid, ta, ta, tb, ta, p, s, pdl))
         e = nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
 #undef I8_ROWS
     } else {
@@ -410,12 +412,14 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     p.M = T;
     p.MB = 1;
     p.active = r.active;
+    p.max_active = A;
     p.ids = ids;
     p.wts = wts;
     p.top_k = top_k;
     p.hq = b + L.hq;
     p.hs = reinterpret_cast<float*>(b + L.hs);
     p.parts = reinterpret_cast<float*>(b + L.parts);
+    p.part_rows = T;
     p.status = reinterpret_cast<int*>(b + L.status);
     p.wait_limit_ns = o.wait_ns;
     p.test_flags = o.test_flags;
@@ -429,9 +433,10 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     g.ws = w->gate_scales;
     g.ws2 = w->up_scales;
     g.tickets = reinterpret_cast<unsigned*>(b + L.t_gate);
-    const int ggrid = fr_shares(A * IB * HB, A * IB, ctas);
-    e = nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, g, s, true)
-                 : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, g, s, true);
+    // (how many experts the tokens reach is known on the device only: blocks past the shares leave)
+    const int ggrid = std::min(ctas, std::max(A * IB, A * IB * HB / kFRMinUnits));
+    e = nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
+                 : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true);
     if (e != cudaSuccess) return cuda_status(e);
     Fp8RowsParams d = p;
     d.N = H;
@@ -444,10 +449,10 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     d.Y = Y;
     d.test_flags = 0;
     d.tickets = reinterpret_cast<unsigned*>(b + L.t_down);
-    const int dgrid = fr_shares(A * IB * HB, HB, ctas);
+    const int dgrid = std::min(ctas, std::max(HB, A * IB * HB / kFRMinUnits));
 #define I8_DOWN(NT)                                                                        \
-    (f16 ? launch_rows<kDown, NT, false, F16>(dev, dgrid, td, td, th, d, s, true)          \
-         : launch_rows<kDown, NT, false, BF16>(dev, dgrid, td, td, th, d, s, true))
+    (f16 ? launch_rows<kDown, NT, false, F16>(dev, dgrid, td, td, th, td, d, s, true)          \
+         : launch_rows<kDown, NT, false, BF16>(dev, dgrid, td, td, th, td, d, s, true))
     e = nt == 32 ? I8_DOWN(32) : I8_DOWN(64);
 #undef I8_DOWN
     return cuda_status(e);

@@ -157,7 +157,72 @@ __device__ __forceinline__ void mma_e4m3_k128(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
-// The same on an SM pair (issued by the even CTA's elected thread).
+// A unit of the weight-streaming kernel in one block: a look at the two
+// barriers that the next unit needs, this unit's MMAs (one 128-byte K block of
+// A against kA boxes of B, 128 accumulator columns apart), and a commit to
+// `done` unless !commit.  Returns the looks' answers (bit 0 `full`, bit 1
+// `empty`).  A look takes ~170 cycles while the tensor core reads shared
+// memory; taken between units, the two set the pace (590 cycles a unit), and
+// only inside one block can their answers be picked up after the MMAs.
+template <int kA>
+__device__ __forceinline__ uint32_t mma_unit(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint64_t* done, bool commit, uint64_t* full, uint32_t pf, uint64_t* empty,
+                                             uint32_t pe) {
+    const uint32_t z = 0, one = 1;
+    uint32_t ra, rb;
+    if constexpr (kA == 1) {
+        asm volatile(
+            "{\n\t.reg .pred p, q, r, s, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 r, [%10], %11;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 s, [%12], %13;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "setp.ne.b32 t, %9, 0;\n\t"
+            "add.s64 a1, %3, 2;\n\tadd.s64 a2, %3, 4;\n\tadd.s64 a3, %3, 6;\n\t"
+            "add.s64 b1, %4, 2;\n\tadd.s64 b2, %4, 4;\n\tadd.s64 b3, %4, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], %3, %4, %5, {%6, %6, %6, %6}, p;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
+            "@t tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t"
+            "selp.u32 %0, 1, 0, r;\n\t"
+            "selp.u32 %1, 2, 0, s;\n\t}\n"
+            : "=r"(ra), "=r"(rb)
+            : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(z), "r"(one), "r"(smem_u32(done)),
+              "r"((uint32_t)commit), "r"(smem_u32(full)), "r"(pf), "r"(smem_u32(empty)), "r"(pe)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p, q, r, s, t;\n\t.reg .b64 a1, a2, a3, b0, b1, b2, b3;\n\t.reg .b32 d;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 r, [%10], %11;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 s, [%12], %13;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "setp.ne.b32 t, %9, 0;\n\t"
+            "add.s64 a1, %3, 2;\n\tadd.s64 a2, %3, 4;\n\tadd.s64 a3, %3, 6;\n\t"
+            "add.s64 b1, %4, 2;\n\tadd.s64 b2, %4, 4;\n\tadd.s64 b3, %4, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], %3, %4, %5, {%6, %6, %6, %6}, p;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
+            "add.u32 d, %2, 128;\n\t"
+            "add.s64 b0, %4, 1024;\n\tadd.s64 b1, %4, 1026;\n\tadd.s64 b2, %4, 1028;\n\tadd.s64 b3, %4, 1030;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], %3, b0, %5, {%6, %6, %6, %6}, p;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
+            "@t tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t"
+            "selp.u32 %0, 1, 0, r;\n\t"
+            "selp.u32 %1, 2, 0, s;\n\t}\n"
+            : "=r"(ra), "=r"(rb)
+            : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(z), "r"(one), "r"(smem_u32(done)),
+              "r"((uint32_t)commit), "r"(smem_u32(full)), "r"(pf), "r"(smem_u32(empty)), "r"(pe)
+            : "memory");
+    }
+    return ra | rb;
+}
+
+// mma_e4m3_k128 on an SM pair (issued by the even CTA's elected thread).
 __device__ __forceinline__ void mma_e4m3_k128_2sm(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
     const uint32_t z = 0, one = 1;
     asm volatile(
@@ -173,6 +238,23 @@ __device__ __forceinline__ void mma_e4m3_k128_2sm(uint32_t d_tmem, uint64_t a_de
             d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(z), "r"(one)
         : "memory");
+}
+
+// Ask for one box of a 3-D tensor in L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// One more at *p; what this thread's block wrote before the last barrier is
+// visible (at GPU scope) to whoever sees this addition, and what others
+// published this way is visible to this thread and, after a barrier, its block.
+__device__ __forceinline__ unsigned ticket_take(unsigned* p) {
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
 }
 
 // 3-D tiled load of one box (x times the element size a multiple of 16).

@@ -45,7 +45,10 @@
 //   the rest    (up to ten) take the units in turn: the unit's scale products
 //               into shared memory, and with kFuse the rows' codes (the rows'
 //               16-bit values are read, quantised and written to the swizzled
-//               A operand).
+//               A operand).  In kGateUp two do that, and the others finish
+//               whole tiles (the epilogue, which sits on one or two schedulers,
+//               would hold up the stream for 8 us a tile with it).
+// At the end all but the first two join the shared tiles, a warp per row.
 #pragma once
 
 #include "fp8_common.cuh"
@@ -68,20 +71,23 @@ struct Fp8RowsParams {
     const float* ws;       // NB x KB (kGateUp, kDown: per expert)
     const float* ws2;      // kGateUp: the up weight's
     const int32_t* active; // kGateUp, kDown: count, then the chosen experts in ascending order
+    int max_active;        // the count is at most this
     const int32_t* ids;    // M x top_k chosen experts and their weights
     const float* wts;
     int top_k;
     void* Y;               // kRows, kDown: M x N, 16 bits
     uint8_t* hq;           // kGateUp: codes [a][M][N], scales [(a * NB + nb) * M + m]
     float* hs;
-    float* parts;          // two slots of kA x 128 x kNT floats per CTA
+    float* parts;          // per CTA two slots (kGateUp: four) of part_rows x kA x 128 floats
+    int part_rows;         // rows of a tile: min(M, kNT)
     unsigned* tickets;     // one per tile, zero between calls
     int* status;
     uint64_t wait_limit_ns;
-    uint32_t test_flags;   // bit 0: block 0 never signals its first accumulator (timeout test)
+    uint32_t test_flags;   // bit 0: block 0 never signals its first unit (timeout test)
 };
 
 constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
+constexpr int kFRPrefetch = 10;  // boxes of the next product fetched into L2 per block (24 MB in all)
 constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
 
 // 16 epilogue warps leave no other below 16
@@ -93,11 +99,11 @@ template <int kMode>
 __host__ __device__ constexpr int fr_bufs() { return 512 / (128 * fr_a<kMode>()); }  // accumulators: all of TMEM
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stage_bytes() { return fr_a<kMode>() * 16384 + kNT * 128; }
-template <int kMode, int kNT>
-__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + 4 * kNT * 4 + (fr_bufs<kMode>() + 1) * 8 + 64; }
+template <int kMode>
+__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + (fr_bufs<kMode>() + 1) * 8 + 64; }
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_bytes(int stages) {
-    return fr_fixed_bytes<kMode, kNT>() + stages * (fr_stage_bytes<kMode, kNT>() + 16) +
+    return fr_fixed_bytes<kMode>() + stages * (fr_stage_bytes<kMode, kNT>() + 16) +
            (stages + fr_bufs<kMode>()) * fr_a<kMode>() * kNT * 4;
 }
 template <int kMode, int kNT>
@@ -109,18 +115,38 @@ __host__ __device__ constexpr int fr_stages() {
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_smem_bytes() { return fr_bytes<kMode, kNT>(fr_stages<kMode, kNT>()); }
 
-// Shares for `units` units in `tiles` tiles on at most `ctas` CTAs.
-__host__ __device__ __forceinline__ int fr_shares(int units, int tiles, int ctas) {
-    const int want = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
-    return want < ctas ? want : ctas;
-}
-
-// The shares: of `per` units each, the first `more` of them one unit more.
+// How `tiles` tiles of kbt units are shared out on at most `ctas` CTAs.  Where
+// cutting every tile in the same number of pieces keeps at least 4 of 5 CTAs
+// busy, that is done (`cut` pieces a tile): a CTA then has a part of one tile
+// only, and one SM's stream (56 GB/s of a matrix that is not in L2, whatever
+// the other SMs do) times 118 is still all that HBM gives.  Otherwise equal
+// runs of units, of `per` units each, the first `more` of them one unit more.
+// A share smaller than kFRMinUnits costs more in joining than it saves.
 // (Units are 16 KB of weight each, so their number is far below 2^31.)
 struct FrShares {
-    int per, more;
-    __device__ __forceinline__ int start(int share) const { return share * per + min(share, more); }
+    int kbt, count, cut, per, more;
+    __host__ __device__ __forceinline__ FrShares(int tiles, int kbt_, int ctas) : kbt(kbt_), cut(0) {
+        const int units = tiles * kbt;
+        int most = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
+        if (most > ctas) most = ctas;
+        const int c = tiles < most ? most / tiles : 0;
+        if (c > 0 && 5 * c * tiles >= 4 * most) cut = c;
+        count = cut ? cut * tiles : most;
+        per = units / count;
+        more = units % count;
+    }
+    __device__ __forceinline__ int start(int share) const {
+        if (cut) {
+            const int t = share / cut;
+            return t * kbt + (share - t * cut) * kbt / cut;
+        }
+        return share * per + min(share, more);
+    }
     __device__ __forceinline__ int owner(int unit) const {
+        if (cut) {
+            const int t = unit / kbt;
+            return t * cut + ((unit - t * kbt + 1) * cut - 1) / kbt;
+        }
         const int big = more * (per + 1);
         return unit < big ? unit / (per + 1) : more + (unit - big) / per;
     }
@@ -141,7 +167,8 @@ __device__ __forceinline__ void pin16(uint64_t (&v)[16]) {
 template <int kMode, int kNT, bool kFuse, typename T>
 __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     k_fp8_rows(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_w2,
-               const __grid_constant__ CUtensorMap tm_x, const Fp8RowsParams p) {
+               const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_next,
+               const Fp8RowsParams p) {
     constexpr int kA = fr_a<kMode>();
     constexpr int kStageBytes = fr_stage_bytes<kMode, kNT>();
     constexpr int kStages = fr_stages<kMode, kNT>();
@@ -150,7 +177,11 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     constexpr int kQ = kNT / 32;                   // TMEM lane quadrants with rows
     constexpr int kEpiThreads = 4 * kQ * 32;
     constexpr int kSpare = fr_threads<kNT>() / 32 - 4 * kQ - 2;  // warps that make scales (and codes):
-    constexpr int kSide = kFuse || kSpare < 4 ? kSpare : 4;      // all of those left over if there are codes to make
+    // all of those left over if there are codes to make; a scale needs fewer
+    constexpr int kSide = kFuse ? kSpare : kMode == kGateUp || kSpare < 4 ? 2 : 4;
+    constexpr int kFin = kMode == kGateUp ? kSpare - kSide : 0;  // warps that finish whole tiles
+    constexpr int kSlotsCta = kMode == kGateUp ? 4 : 2;          // stored sums: shared tiles, whole tiles in turn
+    constexpr int kJoinWarps = fr_threads<kNT>() / 32 - 2;       // (an even number)
     static_assert(kNT == 32 || kNT == 64 || kNT == 128, "rows");
     // a stage's MMAs may complete again only after the epilogue has seen their last completion
     static_assert(kStages > kBufs, "stages");
@@ -166,8 +197,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     // those were issued after the epilogue had read the slot's last content
     // (an accumulator is released only once its scales have been read).
     float* slots = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // [slots][kA][kNT]
-    float* hmax = slots + kSlots * kA * kNT;       // kGateUp: [4][kNT]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(hmax + 4 * kNT);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(slots + kSlots * kA * kNT);
     uint64_t* full = bars;                         // [stages] boxes, rows and scales are there
     uint64_t* done = bars + kStages;               // [stages] the stage's MMAs are complete
     uint64_t* tempty = bars + 2 * kStages;         // [bufs] the epilogue has read the accumulator
@@ -205,52 +235,180 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     const uint32_t tmem_base = *tmem_slot;
 
     // nothing is read before the work ahead on the stream is done, weights
-    // included: a kernel there may have written them
-    pdl_wait();
-    pdl_launch_dependents();
+    // included: a kernel there may have written them.  kDown alone starts on
+    // its weights while the gate/up kernel's last blocks finish: that kernel
+    // lets this one start only after its own wait, when the router and all
+    // before it were done, and writes neither weights nor routing.
+    if (kMode != kDown) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
 
-    const int n_active = kMode == kRows ? 1 : p.active[0];
+    // the chosen experts: their count and the first 31 with one load per warp
+    const int act = kMode == kRows ? 0 : (lane < p.max_active + 1 ? __ldcg(p.active + lane) : 0);
+    const int n_active = kMode == kRows ? 1 : __shfl_sync(0xffffffffu, act, 0);
     const int kbt = kMode == kDown ? p.KB * n_active : p.KB;  // units per tile
     const int tiles = kMode == kRows ? p.NB * p.MB : kMode == kGateUp ? p.NB * n_active : p.NB;
-    const int units = tiles * kbt;
-    const int C = fr_shares(units, tiles, (int)gridDim.x);
     const int c = (int)blockIdx.x;
-    const FrShares sh{units / C, units % C};
+    const FrShares sh(tiles, kbt, (int)gridDim.x);
+    const int C = sh.count;
     const int nu = c < C ? sh.start(c + 1) - sh.start(c) : 0;  // this CTA's units
     const int first_tile = sh.start(c) / kbt, first_kb = sh.start(c) - first_tile * kbt;
+    const size_t slot_floats = (size_t)p.part_rows * kA * 128;
+
+    // Rows row0, row0 + step, ... of a tile from its stored sums: added over
+    // the owners cf .. cl (in the order of k), then the output.  By one warp,
+    // 4 channels per lane.
+    const auto finish_rows = [&](int t, int row0, int step, int cf, int cl, const auto& part_of) {
+        constexpr int kR = 4, kO = kA == 2 ? 1 : 4;  // kR rows' loads of kO owners in flight together
+        const int m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
+        const int nb = kMode == kRows ? t / p.MB : kMode == kGateUp ? t % p.NB : t;
+        const int n = nb * 128 + 4 * lane;
+        const int e = kMode == kGateUp ? __ldcg(p.active + 1 + t / p.NB) : 0;
+#pragma unroll 1
+        for (int r0 = row0; r0 < rows; r0 += step * kR) {
+            float4 sum[kR][kA];
+            int id[kR];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const int row = r0 + r * step;
+                id[r] = kMode == kGateUp && row < rows && lane < p.top_k ? __ldcg(p.ids + row * p.top_k + lane) : -1;
+#pragma unroll
+                for (int a = 0; a < kA; ++a) sum[r][a] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll 1
+            for (int o0 = cf; o0 <= cl; o0 += kO) {
+                float4 x[kO][kR][kA];
+#pragma unroll
+                for (int o = 0; o < kO; ++o) {
+                    const float4* from = reinterpret_cast<const float4*>(part_of(min(o0 + o, cl))) + lane;
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
+                        const int row = r0 + r * step;
+#pragma unroll
+                        for (int a = 0; a < kA; ++a)
+                            x[o][r][a] = o0 + o <= cl && row < rows ? __ldcg(from + (row * kA + a) * 32)
+                                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+#pragma unroll
+                for (int o = 0; o < kO; ++o)
+#pragma unroll
+                    for (int r = 0; r < kR; ++r)
+#pragma unroll
+                        for (int a = 0; a < kA; ++a) {
+                            sum[r][a].x = __fadd_rn(sum[r][a].x, x[o][r][a].x);
+                            sum[r][a].y = __fadd_rn(sum[r][a].y, x[o][r][a].y);
+                            sum[r][a].z = __fadd_rn(sum[r][a].z, x[o][r][a].z);
+                            sum[r][a].w = __fadd_rn(sum[r][a].w, x[o][r][a].w);
+                        }
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const int row = r0 + r * step;
+                if (row >= rows) continue;  // the same for the whole warp
+                if constexpr (kMode == kGateUp) {
+                    const int a = t / p.NB;
+                    const bool chosen = __any_sync(0xffffffffu, id[r] == e);
+                    const float4 g = sum[r][0], up = sum[r][kA - 1];
+                    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (chosen)
+                        h = make_float4(silu_mul(g.x, up.x), silu_mul(g.y, up.y), silu_mul(g.z, up.z), silu_mul(g.w, up.w));
+                    float amax = fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)));
+                    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+                    const float s = fp8_block_scale(amax), inv = __frcp_rn(s);
+                    const uint32_t q =
+                        e4m3x4(__fmul_rn(h.x, inv), __fmul_rn(h.y, inv), __fmul_rn(h.z, inv), __fmul_rn(h.w, inv));
+                    if (n < p.N) *reinterpret_cast<uint32_t*>(p.hq + ((size_t)a * p.M + row) * p.N + n) = q;
+                    if (lane == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? s : 0.0f;
+                } else if (n < p.N) {  // N % 16 == 0
+                    const float4 x = sum[r][0];
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n) =
+                        make_uint2(T::pack(x.x, x.y), T::pack(x.z, x.w));
+                }
+            }
+        }
+    };
 
     if (role == 0) {
         // ------------------------------------------------ TMA producer
+        const int first_a = kMode == kGateUp ? first_tile / p.NB : kMode == kDown ? first_kb / p.KB : 0;
+        const int first_e = __shfl_sync(0xffffffffu, act, (1 + first_a) & 31);
         if (elect_one()) {
             const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0;
-            int tile = first_tile, kb = first_kb;
+            // where the boxes are: k, channel, and expert or row of X; kept up to date with
+            // additions (a division per unit would set the pace of the stream)
+            int kb = first_kb;
+            int nb = kMode == kRows ? first_tile / p.MB : kMode == kGateUp ? first_tile - first_a * p.NB : first_tile;
+            int mb = kMode == kRows ? first_tile - nb * p.MB : 0;
+            int a = first_a, ib = kMode == kDown ? first_kb - first_a * p.KB : 0, e = first_a < 31 ? first_e : __ldcg(p.active + 1 + first_a);
+            // kDown: the rows of the units whose boxes went ahead of the wait
+            const auto early_rows = [&](int n) {
+                pdl_wait();
+                pdl_launch_dependents();
+                int da = first_a, dib = first_kb - first_a * p.KB;
+                for (int j = 0; j < n; ++j) {
+                    tma_load_3d(xring + j * (kNT * 128), &tm_x, &full[j], dib * 128, 0, da, pol_x);
+                    if (++dib == p.KB) {
+                        dib = 0;
+                        if (++da == n_active) da = 0;
+                    }
+                }
+            };
             for (int i = 0; i < nu; ++i) {
-                if (!wait_fast(&done[stage], phase ^ 1, wctx)) break;
+                if (kMode == kDown && i == kStages) early_rows(kStages);
+                if (i >= kStages && !wait_fast(&done[stage], phase ^ 1, wctx)) break;
                 uint8_t* sw = wring + stage * (kA * 16384);
                 uint8_t* sx = xring + stage * (kNT * 128);
                 mbar_arrive_expect_tx(&full[stage], kFuse ? kA * 16384 : kStageBytes);
                 if (kMode == kRows) {
-                    tma_load_2d(sw, &tm_w, &full[stage], kb * 128, (tile / p.MB) * 128, pol_w);
-                    if (!kFuse) tma_load_2d(sx, &tm_x, &full[stage], kb * 128, (tile % p.MB) * kNT, pol_x);
+                    tma_load_2d(sw, &tm_w, &full[stage], kb * 128, nb * 128, pol_w);
+                    if (!kFuse) tma_load_2d(sx, &tm_x, &full[stage], kb * 128, mb * kNT, pol_x);
                 } else if (kMode == kGateUp) {
-                    const int e = p.active[1 + tile / p.NB], nb = tile % p.NB;
                     tma_load_3d(sw, &tm_w, &full[stage], kb * 128, nb * 128, e, pol_w);
                     tma_load_3d(sw + 16384, &tm_w2, &full[stage], kb * 128, nb * 128, e, pol_w);
                     tma_load_2d(sx, &tm_x, &full[stage], kb * 128, 0, pol_x);
                 } else {
-                    const int a = kb / p.KB, ib = kb - a * p.KB;
-                    tma_load_3d(sw, &tm_w, &full[stage], ib * 128, tile * 128, p.active[1 + a], pol_w);
-                    tma_load_3d(sx, &tm_x, &full[stage], ib * 128, 0, a, pol_x);
+                    tma_load_3d(sw, &tm_w, &full[stage], ib * 128, nb * 128, e, pol_w);
+                    if (i >= kStages) tma_load_3d(sx, &tm_x, &full[stage], ib * 128, 0, a, pol_x);
                 }
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1;
                 }
+                if (kMode == kDown && ++ib == p.KB) {
+                    ib = 0;
+                    if (++a == n_active) a = 0;
+                    if (i + 1 < nu) e = __ldcg(p.active + 1 + a);
+                }
                 if (++kb == kbt) {
                     kb = 0;
-                    ++tile;
+                    if (kMode == kRows) {
+                        if (++mb == p.MB) {
+                            mb = 0;
+                            ++nb;
+                        }
+                    } else if (++nb == p.NB && kMode == kGateUp) {
+                        nb = 0;
+                        ++a;
+                        if (i + 1 < nu) e = __ldcg(p.active + 1 + a);
+                    }
+                }
+            }
+            if (kMode == kDown && nu <= kStages) early_rows(nu);
+            if (kMode == kGateUp) {
+                // the down product's first boxes of this block's share, into L2 while the
+                // last tiles are joined and the next kernel starts
+                const int kbd = p.NB * n_active;
+                const FrShares sd(p.KB, kbd, (int)gridDim.x);
+                if (c < sd.count) {
+                    const int end = min(sd.start(c + 1), sd.start(c) + kFRPrefetch);
+                    for (int u = sd.start(c); u < end; ++u) {
+                        const int t = u / kbd, k = u - t * kbd, a = k / p.NB;
+                        tma_prefetch_3d(&tm_next, (k - a * p.NB) * 128, t * 128, __ldcg(p.active + 1 + a));
+                    }
                 }
             }
         }
@@ -260,28 +418,27 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             const uint32_t idesc = idesc_e4m3_f32(128, 128);
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
-            bool issued = false, loaded = false;
+            bool issued = false;
+            uint32_t seen = 0;
             for (int i = 0; i < nu; ++i) {
-                if (!wait_fast(&tempty[buf], buf_phase ^ 1, wctx)) break;
-                if (!loaded && !wait_fast(&full[stage], phase, wctx)) break;
+                if (!(seen & 1u) && !wait_fast(&full[stage], phase, wctx)) break;
+                if (!(seen & 2u) && !wait_fast(&tempty[buf], buf_phase ^ 1, wctx)) break;
                 tc_fence_after();
                 const uint64_t dx = sdesc_k128sw(smem_u32(xring + stage * (kNT * 128)));
-                const uint32_t sw = smem_u32(wring + stage * (kA * 16384));
+                const uint64_t dw = sdesc_k128sw(smem_u32(wring + stage * (kA * 16384)));
                 const uint32_t d = tmem_base + (uint32_t)(buf * kA * 128);
-#pragma unroll
-                for (int a = 0; a < kA; ++a)
-                    mma_e4m3_k128(d + (uint32_t)(a * 128), dx, sdesc_k128sw(sw + a * 16384), idesc);
-                issued = true;
-                if (!((p.test_flags & 1u) && c == 0 && i == 0)) tc_commit(&done[stage]);
+                uint64_t* const dn = &done[stage];
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1;
                 }
-                loaded = mbar_try_wait(&full[stage], phase);  // while this unit's MMAs run
                 if (++buf == kBufs) {
                     buf = 0;
                     buf_phase ^= 1;
                 }
+                seen = mma_unit<kA>(d, dx, dw, idesc, dn, !((p.test_flags & 1u) && c == 0 && i == 0), &full[stage], phase,
+                                    &tempty[buf], buf_phase ^ 1);
+                issued = true;
             }
             if (issued) {  // every MMA has retired before TMEM is freed
                 tc_commit(drain);
@@ -290,13 +447,13 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         }
     } else if (epilogue) {
         // ------------------------------------------------ epilogue
+        if (kMode == kDown) pdl_wait();  // Y, parts and tickets are other kernels' too until then
         const int quad = warp & 3, c0 = (warp >> 2) * 32;  // channels c0 .. c0 + 31 of the tile
         const int row = quad * 32 + lane;
-        const bool lead = warp == 0 && lane == 0;
         int buf = 0, slot = 0, stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        int head_tile = -1, last_tile = -1;  // tiles shared with other CTAs, at the share's start and end
+        int whole_tiles = 0;
         int tile = first_tile, kb = first_kb;
         for (int left = nu; left > 0; ++tile, kb = 0) {
             const int seg = min(kbt - kb, left);  // this share's units of the tile
@@ -307,20 +464,18 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[a][i] = 0;
             for (int i = 0; i < seg; ++i) {
-                float s1[kA];
                 // after a wait that ran out the loops go on without waiting, so
                 // that every barrier and ticket below is still met
                 if (ok) ok = __all_sync(0xffffffffu, wait_fast(&done[stage], phase, wctx));
                 tc_fence_after();
-#pragma unroll
-                for (int a = 0; a < kA; ++a) s1[a] = slots[(slot * kA + a) * kNT + row];
                 const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kA * 128 + c0);
 #pragma unroll
                 for (int a = 0; a < kA; ++a) {
+                    const float s1 = slots[(slot * kA + a) * kNT + row];
                     uint32_t r[32];
                     tmem_ld32(t + (uint32_t)(a * 128), r);
                     tmem_wait_ld32(r);
-                    fma32(v[a], r, f32x2(s1[a], s1[a]));
+                    fma32(v[a], r, f32x2(s1, s1));
                     if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
                 }
                 tc_fence_before();
@@ -337,11 +492,14 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
 
             const int m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
             const bool in = m0 + row < p.M;
-            if (!whole) {
-                // this CTA's sums of the tile, [kNT rows][kA][128 channels]; slot 0 for a
-                // tile that began in an earlier share, slot 1 for one that begins here
+            if (!whole || kMode == kGateUp) {
+                // this CTA's sums of the tile, [rows][kA][128 channels]; slot 0 for a tile that
+                // began in an earlier share, slot 1 for one that begins here and goes on,
+                // slots 2 and 3 for whole ones
+                const int ps = !whole ? (starts ? 1 : 0) : 2 + (whole_tiles & 1);
+                if (kMode == kGateUp && whole && whole_tiles >= 2) named_bar_sync(4 + (whole_tiles & 1), kEpiThreads + 32 * kFin);
                 if (in) {
-                    float4* part = reinterpret_cast<float4*>(p.parts + (size_t)(2 * c + (starts ? 1 : 0)) * (kNT * kA * 128) +
+                    float4* part = reinterpret_cast<float4*>(p.parts + (size_t)(kSlotsCta * c + ps) * slot_floats +
                                                              (size_t)row * (kA * 128) + c0);
 #pragma unroll
                     for (int a = 0; a < kA; ++a)
@@ -351,159 +509,97 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                             __stcg(part + a * 32 + i, make_float4(x.x, x.y, y.x, y.y));
                         }
                 }
-                if (starts)
-                    last_tile = tile;
-                else
-                    head_tile = tile;
+                if (kMode == kGateUp && whole) {
+                    named_bar_arrive(2 + (whole_tiles & 1), kEpiThreads + 32 * kFin);
+                    ++whole_tiles;
+                }
                 continue;
             }
-            if constexpr (kMode == kGateUp) {
-                const int a = tile / p.NB, nb = tile % p.NB, e = p.active[1 + a];
-                float amax = 0.0f;
+            const int n = (kMode == kRows ? tile / p.MB : tile) * 128 + c0;
+            if (in) {
+                uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 g = f32x2_parts(v[0][i]), up = f32x2_parts(v[kA - 1][i]);
-                    const float hx = silu_mul(g.x, up.x), hy = silu_mul(g.y, up.y);
-                    amax = fmaxf(amax, fmaxf(fabsf(hx), fabsf(hy)));
-                    v[0][i] = f32x2(hx, hy);
-                    asm volatile("" : "+l"(v[0][i])::"memory");  // one pair at a time, in few registers
-                }
-                hmax[(c0 / 32) * kNT + row] = amax;
-                named_bar_sync(1, kEpiThreads);
-                amax = fmaxf(fmaxf(hmax[row], hmax[kNT + row]), fmaxf(hmax[2 * kNT + row], hmax[3 * kNT + row]));
-                if (in) {
-                    bool chosen = false;
-                    for (int j = 0; j < p.top_k; ++j) chosen |= p.ids[row * p.top_k + j] == e;
-                    const float s = fp8_block_scale(amax), inv = __frcp_rn(s);
-                    uint8_t* dst = p.hq + ((size_t)a * p.M + row) * p.N + nb * 128 + c0;
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 x = f32x2_parts(v[0][8 * q + 2 * i]), y = f32x2_parts(v[0][8 * q + 2 * i + 1]);
-                            w[i] = chosen ? e4m3x4(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(y.x, inv),
-                                                   __fmul_rn(y.y, inv))
-                                          : 0u;
-                        }
-                        if (nb * 128 + c0 + q * 16 < p.N)  // N % 16 == 0
-                            *reinterpret_cast<uint4*>(dst + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = f32x2_parts(v[0][4 * q + i]);
+                        w[i] = T::pack(f.x, f.y);
                     }
-                    if (c0 == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? s : 0.0f;
-                }
-                named_bar_sync(1, kEpiThreads);  // hmax has been read
-            } else {
-                const int n = (kMode == kRows ? tile / p.MB : tile) * 128 + c0;
-                if (in) {
-                    uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = f32x2_parts(v[0][4 * q + i]);
-                            w[i] = T::pack(f.x, f.y);
-                        }
-                        if (n + q * 8 < p.N)  // N % 16 == 0
-                            *reinterpret_cast<uint4*>(y + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    if (n + q * 8 < p.N)  // N % 16 == 0
+                        *reinterpret_cast<uint4*>(y + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
         }
-        // The shared tiles come last, after the share has been streamed: their
-        // sums are stored by now, and nothing waits for what follows.
-        if (head_tile >= 0 || last_tile >= 0) {
-            __threadfence();
-            named_bar_sync(1, kEpiThreads);
-            if (lead) {
-                int f = 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int t = i == 0 ? head_tile : last_tile;
-                    if (t < 0) continue;
-                    const int others = sh.owner((t + 1) * kbt - 1) - sh.owner(t * kbt);
-                    if (atomicAdd(&p.tickets[t], 1u) == (unsigned)others) {
-                        p.tickets[t] = 0;  // ready for the next call
-                        f |= 1 << i;
-                    }
-                }
-                *last_flag = f;
-            }
-            named_bar_sync(1, kEpiThreads);
-            const int f = *last_flag;
-            if (f) __threadfence();
-            const int ew = (warp >> 2) * kQ + (warp & 3);  // 0 .. 4 kQ - 1: a warp per row, 4 channels per lane
-#pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                if (!((f >> i) & 1)) continue;
-                const int t = i == 0 ? head_tile : last_tile;
-                const int cf = sh.owner(t * kbt), cl = sh.owner((t + 1) * kbt - 1);
-                const int m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
-                const int nb = kMode == kRows ? t / p.MB : kMode == kGateUp ? t % p.NB : t;
-                const int n = nb * 128 + 4 * lane;
-                constexpr int kR = 4;  // rows whose loads are in flight together
-#pragma unroll 1
-                for (int r0 = ew; r0 < rows; r0 += 4 * kQ * kR) {
-                    float4 sum[kR][kA];
-#pragma unroll
-                    for (int r = 0; r < kR; ++r)
-#pragma unroll
-                        for (int a = 0; a < kA; ++a) sum[r][a] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int o = cf; o <= cl; ++o) {  // in the order of k
-                        const float4* from =
-                            reinterpret_cast<const float4*>(p.parts + (size_t)(2 * o + (sh.start(o) <= t * kbt ? 1 : 0)) *
-                                                                          (kNT * kA * 128)) + lane;
-#pragma unroll
-                        for (int r = 0; r < kR; ++r) {
-                            const int row = r0 + r * 4 * kQ;
-                            if (row < rows) {
-#pragma unroll
-                                for (int a = 0; a < kA; ++a) {
-                                    const float4 x = __ldcg(from + (row * kA + a) * 32);
-                                    sum[r][a].x = __fadd_rn(sum[r][a].x, x.x);
-                                    sum[r][a].y = __fadd_rn(sum[r][a].y, x.y);
-                                    sum[r][a].z = __fadd_rn(sum[r][a].z, x.z);
-                                    sum[r][a].w = __fadd_rn(sum[r][a].w, x.w);
-                                }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < kR; ++r) {
-                        const int row = r0 + r * 4 * kQ;
-                        if (row >= rows) continue;  // the same for the whole warp
-                        if constexpr (kMode == kGateUp) {
-                            const int a = t / p.NB, e = p.active[1 + a];
-                            const float4 g = sum[r][0], up = sum[r][kA - 1];
-                            const float4 h = make_float4(silu_mul(g.x, up.x), silu_mul(g.y, up.y), silu_mul(g.z, up.z),
-                                                         silu_mul(g.w, up.w));
-                            float amax = fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)));
-#pragma unroll
-                            for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-                            const bool chosen = __any_sync(0xffffffffu, lane < p.top_k && p.ids[row * p.top_k + lane] == e);
-                            const float s = fp8_block_scale(amax), inv = __frcp_rn(s);
-                            const uint32_t q = chosen ? e4m3x4(__fmul_rn(h.x, inv), __fmul_rn(h.y, inv),
-                                                               __fmul_rn(h.z, inv), __fmul_rn(h.w, inv))
-                                                      : 0u;
-                            if (n < p.N) *reinterpret_cast<uint32_t*>(p.hq + ((size_t)a * p.M + row) * p.N + n) = q;
-                            if (lane == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? s : 0.0f;
-                        } else if (n < p.N) {  // N % 16 == 0
-                            const float4 x = sum[r][0];
-                            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n) =
-                                make_uint2(T::pack(x.x, x.y), T::pack(x.z, x.w));
-                        }
-                    }
-                }
-            }
+    } else if (kFin > 0 && role >= 2 + kSide) {
+        // ------------------------------------------------ whole tiles of the gated layer
+        int tile = first_tile, kb = first_kb, n = 0;
+        for (int left = nu; left > 0; ++tile, kb = 0) {
+            const int seg = min(kbt - kb, left);
+            left -= seg;
+            if (seg != kbt) continue;
+            named_bar_sync(2 + (n & 1), kEpiThreads + 32 * kFin);  // its sums are stored
+            const float* part = p.parts + (size_t)(kSlotsCta * c + 2 + (n & 1)) * slot_floats;
+            finish_rows(tile, role - 2 - kSide, kFin > 0 ? kFin : 1, 0, 0, [&](int) { return part; });
+            // the slot may be filled again (by the tile after the next, if that one is whole)
+            if (left >= 2 * kbt) named_bar_arrive(4 + (n & 1), kEpiThreads + 32 * kFin);
+            ++n;
         }
     } else {
         // ------------------------------------------------ scales, and codes with kFuse
         const int sidx = role - 2;
-        int tile = first_tile, kb = first_kb + sidx;
-        while (kb >= kbt) {
-            kb -= kbt;
-            ++tile;
-        }
+        int kb = first_kb + sidx;
+        int nb = kMode == kRows ? first_tile / p.MB : kMode == kGateUp ? first_tile % p.NB : first_tile;
+        int mb = kMode == kRows ? first_tile - nb * p.MB : 0, a = kMode == kGateUp ? first_tile / p.NB : 0;
+        const auto settle = [&]() {  // kb counts on from a tile's start: to the tile that it is in
+            while (kb >= kbt) {
+                kb -= kbt;
+                if (kMode == kRows) {
+                    if (++mb == p.MB) {
+                        mb = 0;
+                        ++nb;
+                    }
+                } else if (++nb == p.NB && kMode == kGateUp) {
+                    nb = 0;
+                    ++a;
+                }
+            }
+        };
+        settle();
+        if (kMode == kDown) pdl_wait();
+        // unless kFuse: scales of the rows and of the boxes, and routing weights, of the unit at kb
+        float ax[kQ], ar[kQ], aw = 0.0f, aw2 = 0.0f;
+        int we = -1;  // kDown: the expert that ar is of
+        const auto load = [&]() {
+            const float* xs = p.xs + kb * p.xs_pitch + mb * kNT;
+            size_t o = (size_t)nb * p.KB + kb;
+            if (kMode == kGateUp) o += (size_t)__ldcg(p.active + 1 + a) * p.NB * p.KB;
+            if (kMode == kDown) {
+                const int d = kb / p.KB, ib = kb - d * p.KB, e = __ldcg(p.active + 1 + d);
+                o = ((size_t)e * p.NB + nb) * p.KB + ib;
+                if (e != we) {
+                    we = e;
+#pragma unroll
+                    for (int j = 0; j < kQ; ++j) {
+                        const int m = lane + 32 * j;
+                        ar[j] = 0.0f;  // the token's weight for this expert
+                        if (m < p.M)
+                            for (int q = 0; q < p.top_k; ++q)
+                                if (__ldcg(p.ids + m * p.top_k + q) == e) ar[j] = __ldcg(p.wts + m * p.top_k + q);
+                    }
+                }
+            }
+            aw = __ldg(p.ws + o);
+            if (kA == 2) aw2 = __ldg(p.ws2 + o);
+#pragma unroll
+            for (int j = 0; j < kQ; ++j) {
+                const int m = lane + 32 * j;
+                ax[j] = mb * kNT + m < p.M ? xs[m] : 0.0f;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) ax[j] = 0.0f, ar[j] = 1.0f;
+        if (!kFuse && sidx < kSide && sidx < nu) load();
         for (int i = sidx < kSide ? sidx : nu; i < nu; i += kSide) {
             const int stage = i % kStages, slot = i % kSlots;
             const uint32_t phase = (uint32_t)(i / kStages) & 1u;
@@ -527,7 +623,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         }
                     }
                 }
-                const float w = __ldg(p.ws + (size_t)tile * p.KB + kb);
+                const float w = __ldg(p.ws + (size_t)nb * p.KB + kb);
                 if (!__all_sync(0xffffffffu, wait_fast(&done[stage], phase ^ 1, wctx))) break;
                 uint8_t* sx = xring + stage * (kNT * 128);
 #pragma unroll
@@ -546,34 +642,12 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 }
                 fence_proxy_async_smem();
             } else {
-                float f[kQ], g[kQ];
+                float f[kQ], g[kQ];  // this unit's products; the next one's are loaded meanwhile
 #pragma unroll
-                for (int j = 0; j < kQ; ++j) {
-                    const int m = lane + 32 * j;
-                    f[j] = g[j] = 0.0f;
-                    if (kMode == kRows) {
-                        const int r = (tile % p.MB) * kNT + m;
-                        if (r < p.M)
-                            f[j] = __fmul_rn(p.xs[kb * p.xs_pitch + r], __ldg(p.ws + (size_t)(tile / p.MB) * p.KB + kb));
-                    } else if (kMode == kGateUp) {
-                        const int e = p.active[1 + tile / p.NB], nb = tile % p.NB;
-                        if (m < p.M) {
-                            const float xs = p.xs[kb * p.xs_pitch + m];
-                            const size_t o = ((size_t)e * p.NB + nb) * p.KB + kb;
-                            f[j] = __fmul_rn(xs, __ldg(p.ws + o));
-                            g[j] = __fmul_rn(xs, __ldg(p.ws2 + o));
-                        }
-                    } else {
-                        const int a = kb / p.KB, ib = kb - a * p.KB, e = p.active[1 + a];
-                        if (m < p.M) {
-                            float w = 0.0f;  // the token's weight for this expert
-                            for (int q = 0; q < p.top_k; ++q)
-                                if (p.ids[m * p.top_k + q] == e) w = p.wts[m * p.top_k + q];
-                            f[j] = __fmul_rn(__fmul_rn(p.xs[((long long)a * p.KB + ib) * p.xs_pitch + m],
-                                                       __ldg(p.ws + ((size_t)e * p.NB + tile) * p.KB + ib)), w);
-                        }
-                    }
-                }
+                for (int j = 0; j < kQ; ++j) f[j] = __fmul_rn(ax[j], aw * ar[j]), g[j] = __fmul_rn(ax[j], aw2);
+                kb += kSide;
+                settle();
+                if (i + kSide < nu) load();
                 if (!__all_sync(0xffffffffu, wait_fast(&done[stage], phase ^ 1, wctx))) break;
 #pragma unroll
                 for (int j = 0; j < kQ; ++j) {
@@ -583,11 +657,43 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[stage]);
-            kb += kSide;
-            while (kb >= kbt) {
-                kb -= kbt;
-                ++tile;
+            if (kFuse) {
+                kb += kSide;
+                settle();
             }
+        }
+    }
+
+    // The tiles that this share holds only a part of come last, after it has
+    // been streamed: the sums are stored by now, and nothing waits for this.
+    const int end_kb = first_kb + nu;  // the share's end, in units from its first tile's start
+    const int head_tile = nu > 0 && first_kb > 0 ? first_tile : -1;
+    const int tail_tile =
+        nu > 0 && end_kb % kbt != 0 && (first_kb == 0 || end_kb > kbt) ? first_tile + end_kb / kbt : -1;
+    if (role != 0 && role != 1 && (head_tile >= 0 || tail_tile >= 0)) {
+        named_bar_sync(1, 32 * kJoinWarps);
+        if (warp == 0) {  // lane 0: the head's ticket, lane 1: the tail's
+            const int t = lane == 0 ? head_tile : lane == 1 ? tail_tile : -1;
+            bool last = false;
+            if (t >= 0) {
+                const int others = sh.owner((t + 1) * kbt - 1) - sh.owner(t * kbt);
+                last = ticket_take(&p.tickets[t]) == (unsigned)others;
+                if (last) p.tickets[t] = 0;  // ready for the next call
+            }
+            const unsigned f = __ballot_sync(0xffffffffu, last);
+            if (lane == 0) *last_flag = (int)f;
+        }
+        named_bar_sync(1, 32 * kJoinWarps);
+        const int f = *last_flag;
+        const int jw = epilogue ? (warp >> 2) * kQ + (warp & 3) : 4 * kQ + role - 2;  // 0 .. kJoinWarps - 1
+        if (f) {
+            // one tile: a row per warp; two: half of the warps each
+            const bool both = f == 3;
+            const int t = f == 1 || (both && (jw & 1) == 0) ? head_tile : tail_tile;
+            finish_rows(t, both ? jw >> 1 : jw, both ? kJoinWarps / 2 : kJoinWarps, sh.owner(t * kbt),
+                        sh.owner((t + 1) * kbt - 1), [&](int o) {
+                            return p.parts + (size_t)(kSlotsCta * o + (sh.start(o) <= t * kbt ? 1 : 0)) * slot_floats;
+                        });
         }
     }
 

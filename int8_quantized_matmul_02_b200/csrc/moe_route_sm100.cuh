@@ -112,16 +112,15 @@ __global__ void __launch_bounds__(kRouteThreads)
         for (int w = 0; w < kRouteThreads / 32; ++w) a += red[w][tid];
         if (e < p.E && t < p.T) __stcg(p.logits + (size_t)t * p.E + e, a);
     }
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
-        const bool last = atomicAdd(&p.tickets[tg], 1u) == (unsigned)(eb - 1);
+        const bool last = ticket_take(&p.tickets[tg]) == (unsigned)(eb - 1);
         if (last) p.tickets[tg] = 0;
         s_last = last;
     }
+    for (int e = tid; e < kMaxExperts; e += kRouteThreads) flags[e] = 0;
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
 
     // the experts of token t0 + warp
     if (warp < kTT && t0 + warp < p.T) {
@@ -183,21 +182,21 @@ __global__ void __launch_bounds__(kRouteThreads)
         if (lane < p.top_k) {
             __stcg(p.ids + (size_t)t * p.top_k + lane, mine_id);
             __stcg(p.wts + (size_t)t * p.top_k + lane, __fdiv_rn(mine, sum));
+            flags[mine_id] = 1;  // all there is to list if these are the only tokens
         }
     }
-    __threadfence();
-    __syncthreads();
     const int groups = (p.T + kTT - 1) / kTT;
-    if (tid == 0) {
-        const bool last = atomicAdd(&p.tickets[groups], 1u) == (unsigned)(groups - 1);
-        if (last) p.tickets[groups] = 0;
-        s_last = last;
-    }
-    for (int e = tid; e < kMaxExperts; e += kRouteThreads) flags[e] = 0;
     __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    for (int i = tid; i < p.T * p.top_k; i += kRouteThreads) flags[__ldcg(p.ids + i)] = 1;
+    if (groups > 1) {
+        if (tid == 0) {
+            const bool last = ticket_take(&p.tickets[groups]) == (unsigned)(groups - 1);
+            if (last) p.tickets[groups] = 0;
+            s_last = last;
+        }
+        __syncthreads();
+        if (!s_last) return;
+        for (int i = tid; i < p.T * p.top_k; i += kRouteThreads) flags[__ldcg(p.ids + i)] = 1;
+    }
     __syncthreads();
     if (warp == 0) {
         int n = 0;
