@@ -10,7 +10,7 @@ constexpr int kMoeMaxTopK = 16;
 bool dtype_ok(int dtype) { return dtype == INT8MM_F16 || dtype == INT8MM_BF16; }
 
 // Rows per tile of the weight-streaming kernel for M rows.
-int fp8_rows_nt(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+int fp8_rows_nt(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 struct Fp8Layout {
     size_t codes, scales, total;
@@ -272,7 +272,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
     const bool f16 = dtype == INT8MM_F16, timed = o.ev0 != nullptr;
     const bool rows = o.path == INT8MM_PATH_DECODE || (o.path == INT8MM_PATH_AUTO && fp8_rows_path(M, N, sms));
     const int nt = fp8_rows_nt(M);
-    const bool fuse = rows && nt == 32;
+    const bool fuse = rows && nt <= 32;
     cudaError_t e = cudaSuccess;
     if (!fuse) e = launch_quant_fp8(X, dtype, M, K, xq, xs, 1, fp8_pitch(M), info->sm_count, s);
     if (e != cudaSuccess) return cuda_status(e);
@@ -306,7 +306,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
 #define I8_ROWS(NT, FUSE)                                                                           \
     (f16 ? launch_rows<kRows, NT, FUSE, F16>(dev, grid, ta, ta, tb, ta, p, s, pdl)                  \
          : launch_rows<kRows, NT, FUSE, BF16>(dev, grid, ta, ta, tb, ta, p, s, pdl))
-        e = nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
+        e = nt == 16 ? I8_ROWS(16, true) : nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
 #undef I8_ROWS
     } else {
         constexpr int bn = 256;
@@ -435,8 +435,9 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     g.tickets = reinterpret_cast<unsigned*>(b + L.t_gate);
     // (how many experts the tokens reach is known on the device only: blocks past the shares leave)
     const int ggrid = std::min(ctas, std::max(A * IB, A * IB * HB / kFRMinUnits));
-    e = nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
-                 : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true);
+    e = nt == 16   ? launch_rows<kGateUp, 16, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
+        : nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
+                   : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true);
     if (e != cudaSuccess) return cuda_status(e);
     Fp8RowsParams d = p;
     d.N = H;
@@ -453,7 +454,7 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
 #define I8_DOWN(NT)                                                                        \
     (f16 ? launch_rows<kDown, NT, false, F16>(dev, dgrid, td, td, th, td, d, s, true)          \
          : launch_rows<kDown, NT, false, BF16>(dev, dgrid, td, td, th, td, d, s, true))
-    e = nt == 32 ? I8_DOWN(32) : I8_DOWN(64);
+    e = nt == 16 ? I8_DOWN(16) : nt == 32 ? I8_DOWN(32) : I8_DOWN(64);
 #undef I8_DOWN
     return cuda_status(e);
 }

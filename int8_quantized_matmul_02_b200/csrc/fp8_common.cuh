@@ -158,13 +158,20 @@ __device__ __forceinline__ void mma_e4m3_k128(uint32_t d_tmem, uint64_t a_desc, 
 }
 
 // A unit of the weight-streaming kernel in one block: a look at the two
-// barriers that the next unit needs, this unit's MMAs (one 128-byte K block of
-// A against kA boxes of B, 128 accumulator columns apart), and a commit to
-// `done` unless !commit.  Returns the looks' answers (bit 0 `full`, bit 1
-// `empty`).  A look takes ~170 cycles while the tensor core reads shared
-// memory; taken between units, the two set the pace (590 cycles a unit), and
-// only inside one block can their answers be picked up after the MMAs.
-template <int kA>
+// barriers that the next unit needs, this unit's MMAs, and a commit to `done`
+// unless !commit.  kA boxes of one operand (16 KB apart: the A operand if
+// kBoxA, else B) against the other, kCols accumulator columns each.  Returns
+// the looks' answers (bit 0 `full`, bit 1 `empty`): a look takes ~170 cycles
+// while the tensor core reads shared memory, and only inside one block can its
+// answer be picked up after the MMAs.
+#define I8MM_MMA4(D, A, B)                                                                \
+    "add.s64 a1, " A ", 2;\n\tadd.s64 a2, " A ", 4;\n\tadd.s64 a3, " A ", 6;\n\t"         \
+    "add.s64 b1, " B ", 2;\n\tadd.s64 b2, " B ", 4;\n\tadd.s64 b3, " B ", 6;\n\t"         \
+    "tcgen05.mma.cta_group::1.kind::f8f6f4 [" D "], " A ", " B ", %5, {%6, %6, %6, %6}, p;\n\t" \
+    "tcgen05.mma.cta_group::1.kind::f8f6f4 [" D "], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"       \
+    "tcgen05.mma.cta_group::1.kind::f8f6f4 [" D "], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"       \
+    "tcgen05.mma.cta_group::1.kind::f8f6f4 [" D "], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
+template <int kA, int kCols, bool kBoxA>
 __device__ __forceinline__ uint32_t mma_unit(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint64_t* done, bool commit, uint64_t* full, uint32_t pf, uint64_t* empty,
                                              uint32_t pe) {
@@ -175,52 +182,34 @@ __device__ __forceinline__ uint32_t mma_unit(uint32_t d_tmem, uint64_t a_desc, u
             "{\n\t.reg .pred p, q, r, s, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 r, [%10], %11;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 s, [%12], %13;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "setp.ne.b32 q, %7, 0;\n\t"
-            "setp.ne.b32 t, %9, 0;\n\t"
-            "add.s64 a1, %3, 2;\n\tadd.s64 a2, %3, 4;\n\tadd.s64 a3, %3, 6;\n\t"
-            "add.s64 b1, %4, 2;\n\tadd.s64 b2, %4, 4;\n\tadd.s64 b3, %4, 6;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], %3, %4, %5, {%6, %6, %6, %6}, p;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\tsetp.ne.b32 t, %9, 0;\n\t"
+            I8MM_MMA4("%2", "%3", "%4")
             "@t tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t"
-            "selp.u32 %0, 1, 0, r;\n\t"
-            "selp.u32 %1, 2, 0, s;\n\t}\n"
+            "selp.u32 %0, 1, 0, r;\n\tselp.u32 %1, 2, 0, s;\n\t}\n"
             : "=r"(ra), "=r"(rb)
             : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(z), "r"(one), "r"(smem_u32(done)),
               "r"((uint32_t)commit), "r"(smem_u32(full)), "r"(pf), "r"(smem_u32(empty)), "r"(pe)
             : "memory");
     } else {
         asm volatile(
-            "{\n\t.reg .pred p, q, r, s, t;\n\t.reg .b64 a1, a2, a3, b0, b1, b2, b3;\n\t.reg .b32 d;\n\t"
+            "{\n\t.reg .pred p, q, r, s, t;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t.reg .b32 d;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 r, [%10], %11;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 s, [%12], %13;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "setp.ne.b32 q, %7, 0;\n\t"
-            "setp.ne.b32 t, %9, 0;\n\t"
-            "add.s64 a1, %3, 2;\n\tadd.s64 a2, %3, 4;\n\tadd.s64 a3, %3, 6;\n\t"
-            "add.s64 b1, %4, 2;\n\tadd.s64 b2, %4, 4;\n\tadd.s64 b3, %4, 6;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], %3, %4, %5, {%6, %6, %6, %6}, p;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%2], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
-            "add.u32 d, %2, 128;\n\t"
-            "add.s64 b0, %4, 1024;\n\tadd.s64 b1, %4, 1026;\n\tadd.s64 b2, %4, 1028;\n\tadd.s64 b3, %4, 1030;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], %3, b0, %5, {%6, %6, %6, %6}, p;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], a1, b1, %5, {%6, %6, %6, %6}, q;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], a2, b2, %5, {%6, %6, %6, %6}, q;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [d], a3, b3, %5, {%6, %6, %6, %6}, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\tsetp.ne.b32 t, %9, 0;\n\t"
+            I8MM_MMA4("%2", "%3", "%4")
+            "add.u32 d, %2, %14;\n\tadd.s64 a0, %3, %15;\n\tadd.s64 b0, %4, %16;\n\t"
+            I8MM_MMA4("d", "a0", "b0")
             "@t tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t"
-            "selp.u32 %0, 1, 0, r;\n\t"
-            "selp.u32 %1, 2, 0, s;\n\t}\n"
+            "selp.u32 %0, 1, 0, r;\n\tselp.u32 %1, 2, 0, s;\n\t}\n"
             : "=r"(ra), "=r"(rb)
             : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(z), "r"(one), "r"(smem_u32(done)),
-              "r"((uint32_t)commit), "r"(smem_u32(full)), "r"(pf), "r"(smem_u32(empty)), "r"(pe)
+              "r"((uint32_t)commit), "r"(smem_u32(full)), "r"(pf), "r"(smem_u32(empty)), "r"(pe), "n"(kCols),
+              "n"(kBoxA ? 1024 : 0), "n"(kBoxA ? 0 : 1024)
             : "memory");
     }
     return ra | rb;
 }
+#undef I8MM_MMA4
 
 // mma_e4m3_k128 on an SM pair (issued by the even CTA's elected thread).
 __device__ __forceinline__ void mma_e4m3_k128_2sm(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {

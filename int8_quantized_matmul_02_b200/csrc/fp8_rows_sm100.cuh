@@ -5,15 +5,21 @@
 //   out[m, n] = sum_b (xs[m, b] * ws[n / 128, b]) * sum_{k in block b} xq[m, k] * wq[n, k]
 //
 // A unit of work is one 128-channel x 128-k box of the weight (16 KB, one
-// scale block; two boxes in the gated layer) with the rows' 128 k.  The rows
-// are the A operand of tcgen05.mma (M = 128, of which only kNT rows are
-// staged: what the tensor core reads past them makes accumulator rows that
-// nobody reads), the channels are B (N = 128).  A unit's sums go to one of the
-// TMEM accumulators in rotation; the epilogue thread of row m (TMEM lane m)
-// adds them, times one scale, to running fp32 sums in registers.  (With the
-// operands the other way round a thread owns a channel and needs every row's
-// scale: the shared-memory reads of those, 16 bytes a time, slowed the tensor
-// core's own reads to 2400 cycles a unit for 128 rows, against 260.)
+// scale block; two boxes in the gated layer) with the rows' 128 k.  A unit's
+// sums go to one of the TMEM accumulators in rotation, and the epilogue adds
+// them, scaled, to running fp32 sums in registers.  Which operand the box is
+// depends on the number of rows:
+//   kNT <= 32 rows: the box is A of tcgen05.mma (M = 128 channels), the rows B
+//     (N = kNT).  An epilogue thread owns a channel and reads every row's scale
+//     from shared memory, 16 bytes a time.  The other way round the tensor core
+//     multiplies 128 rows for the sake of a few, and that is power: a single
+//     token through 12288 x 49152 took 97 us cold, but 117 us in a long run, at
+//     1.05 GHz under the power cap.
+//   kNT >= 64: the rows are A (M = 128, of which only kNT are staged: what is
+//     read past them makes accumulator rows that nobody reads), the box B
+//     (N = 128).  An epilogue thread owns a row and reads one scale.  (The
+//     scales of 64 or 128 rows, read by every thread, slowed the tensor core's
+//     own reads of shared memory to 2400 cycles a unit, against 260.)
 //
 // The units, ordered by output tile and then k, are cut into equal consecutive
 // shares, one per CTA (one CTA per SM), whatever the shape: a CTA's share may
@@ -35,10 +41,9 @@
 // In the gated layer every token is a row for every expert; tokens that did
 // not choose an expert have zero codes and scales there.
 //
-// Warps: with rows in kQ of the four TMEM lane quadrants, the warps w with
-// w % 4 < kQ (w < 16) are the epilogue, one for each quadrant and quarter of
-// the channels (32 sums per thread and box: one load of 32 columns and 16
-// paired FMAs per unit, which keeps well below a unit's time); of the others
+// Warps: the epilogue is warps 0-3 (a TMEM lane quadrant of channels each) for
+// kNT <= 32; above, with rows in kQ quadrants, the warps w with w % 4 < kQ
+// (w < 16), one for each quadrant and quarter of the channels.  Of the others
 //   the first   is the TMA producer of the weight boxes (and of the rows
 //               unless kFuse);
 //   the second  allocates TMEM and issues the MMAs;
@@ -95,16 +100,18 @@ template <int kNT>
 __host__ __device__ constexpr int fr_threads() { return kNT == 128 ? 640 : 512; }
 template <int kMode>
 __host__ __device__ constexpr int fr_a() { return kMode == kGateUp ? 2 : 1; }
-template <int kMode>
-__host__ __device__ constexpr int fr_bufs() { return 512 / (128 * fr_a<kMode>()); }  // accumulators: all of TMEM
+template <int kNT>
+__host__ __device__ constexpr int fr_cols() { return kNT <= 32 ? kNT : 128; }  // accumulator columns of a box
+template <int kMode, int kNT>
+__host__ __device__ constexpr int fr_bufs() { return kNT <= 32 ? 4 : 512 / (128 * fr_a<kMode>()); }  // accumulators
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stage_bytes() { return fr_a<kMode>() * 16384 + kNT * 128; }
-template <int kMode>
-__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + (fr_bufs<kMode>() + 1) * 8 + 64; }
+template <int kMode, int kNT>
+__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + (fr_bufs<kMode, kNT>() + 1) * 8 + 64; }
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_bytes(int stages) {
-    return fr_fixed_bytes<kMode>() + stages * (fr_stage_bytes<kMode, kNT>() + 16) +
-           (stages + fr_bufs<kMode>()) * fr_a<kMode>() * kNT * 4;
+    return fr_fixed_bytes<kMode, kNT>() + stages * (fr_stage_bytes<kMode, kNT>() + 16) +
+           (stages + fr_bufs<kMode, kNT>()) * fr_a<kMode>() * kNT * 4;
 }
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stages() {
@@ -157,6 +164,24 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
 }
 
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+
+// v[0 .. 2 kQuads - 1] (4 kQuads sums) += r * s, a scale for each.
+template <int kQuads>
+__device__ __forceinline__ void fma_scaled(uint64_t* v, const uint32_t* r, const ulonglong2* s) {
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+        const ulonglong2 f = s[i];
+        fma_f32x2(v[2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
+        fma_f32x2(v[2 * i + 1], f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
+    }
+}
+
 // Nothing that follows is moved before the computation of v, nor that after it.
 __device__ __forceinline__ void pin16(uint64_t (&v)[16]) {
     asm volatile("" : "+l"(v[0]), "+l"(v[1]), "+l"(v[2]), "+l"(v[3]), "+l"(v[4]), "+l"(v[5]), "+l"(v[6]), "+l"(v[7]),
@@ -172,17 +197,21 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     constexpr int kA = fr_a<kMode>();
     constexpr int kStageBytes = fr_stage_bytes<kMode, kNT>();
     constexpr int kStages = fr_stages<kMode, kNT>();
-    constexpr int kBufs = fr_bufs<kMode>();
+    constexpr int kBufs = fr_bufs<kMode, kNT>();
     constexpr int kSlots = kStages + kBufs;
-    constexpr int kQ = kNT / 32;                   // TMEM lane quadrants with rows
-    constexpr int kEpiThreads = 4 * kQ * 32;
-    constexpr int kSpare = fr_threads<kNT>() / 32 - 4 * kQ - 2;  // warps that make scales (and codes):
+    constexpr bool kBoxA = kNT <= 32;              // the box is the A operand
+    constexpr int kCols = fr_cols<kNT>();
+    constexpr uint32_t kTmemCols = kBufs * kA * kCols;
+    constexpr int kQ = kNT / 32;                   // !kBoxA: TMEM lane quadrants with rows
+    constexpr int kEpiWarps = kBoxA ? 4 : 4 * kQ, kEpiThreads = 32 * kEpiWarps;
+    constexpr int kSpare = fr_threads<kNT>() / 32 - kEpiWarps - 2;  // warps that make scales (and codes):
     // all of those left over if there are codes to make; a scale needs fewer
     constexpr int kSide = kFuse ? kSpare : kMode == kGateUp || kSpare < 4 ? 2 : 4;
     constexpr int kFin = kMode == kGateUp ? kSpare - kSide : 0;  // warps that finish whole tiles
     constexpr int kSlotsCta = kMode == kGateUp ? 4 : 2;          // stored sums: shared tiles, whole tiles in turn
     constexpr int kJoinWarps = fr_threads<kNT>() / 32 - 2;       // (an even number)
-    static_assert(kNT == 32 || kNT == 64 || kNT == 128, "rows");
+    static_assert(kNT == 16 || kNT == 32 || kNT == 64 || kNT == 128, "rows");
+    static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
     // a stage's MMAs may complete again only after the epilogue has seen their last completion
     static_assert(kStages > kBufs, "stages");
     // a side warp waits for the stage's last completion by parity, so it must not be two rounds
@@ -190,7 +219,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     static_assert(kSide <= kStages, "side warps");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* xring = smem;                         // [stages][kNT rows]; M = 128 reads run on into wring
+    uint8_t* xring = smem;                         // [stages][kNT rows]; reads of M = 128 rows run on into wring
     uint8_t* wring = smem + kStages * kNT * 128;   // [stages][kA boxes]
     // scale products of the units in flight.  A slot is rewritten kSlots units
     // later; its writer has seen the MMAs of kStages units earlier done, and
@@ -207,9 +236,9 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     volatile int* last_flag = abort_flag + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool epilogue = warp < 16 && (warp & 3) < kQ;
+    const bool epilogue = kBoxA ? warp < 4 : warp < 16 && (warp & 3) < kQ;
     // the others, counted: 0 producer, 1 MMA issuer, 2 and on side warps
-    const int role = epilogue ? -1 : warp >= 16 ? warp - 16 : (warp >> 2) * (4 - kQ) + (warp & 3) - kQ;
+    const int role = epilogue ? -1 : kBoxA ? warp - 4 : warp >= 16 ? warp - 16 : (warp >> 2) * (4 - kQ) + (warp & 3) - kQ;
     WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
     if (threadIdx.x == 0) {
@@ -217,7 +246,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             mbar_init(&full[s], 2);  // the producer's expected bytes and the side warp
             mbar_init(&done[s], 1);
         }
-        for (int b = 0; b < kBufs; ++b) mbar_init(&tempty[b], 4 * kQ);
+        for (int b = 0; b < kBufs; ++b) mbar_init(&tempty[b], kEpiWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -226,7 +255,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         if (!kFuse) prefetch_tmap(&tm_x);
     }
     if (role == 1) {
-        tmem_alloc(tmem_slot, 512);
+        tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -415,7 +444,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     } else if (role == 1) {
         // ------------------------------------------------ MMA issuer
         if (elect_one()) {
-            const uint32_t idesc = idesc_e4m3_f32(128, 128);
+            const uint32_t idesc = idesc_e4m3_f32(128, kCols);
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             bool issued = false;
@@ -426,7 +455,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 tc_fence_after();
                 const uint64_t dx = sdesc_k128sw(smem_u32(xring + stage * (kNT * 128)));
                 const uint64_t dw = sdesc_k128sw(smem_u32(wring + stage * (kA * 16384)));
-                const uint32_t d = tmem_base + (uint32_t)(buf * kA * 128);
+                const uint32_t d = tmem_base + (uint32_t)(buf * kA * kCols);
                 uint64_t* const dn = &done[stage];
                 if (++stage == kStages) {
                     stage = 0;
@@ -436,8 +465,9 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                     buf = 0;
                     buf_phase ^= 1;
                 }
-                seen = mma_unit<kA>(d, dx, dw, idesc, dn, !((p.test_flags & 1u) && c == 0 && i == 0), &full[stage], phase,
-                                    &tempty[buf], buf_phase ^ 1);
+                seen = mma_unit<kA, kCols, kBoxA>(d, kBoxA ? dw : dx, kBoxA ? dx : dw, idesc, dn,
+                                                  !((p.test_flags & 1u) && c == 0 && i == 0), &full[stage], phase,
+                                                  &tempty[buf], buf_phase ^ 1);
                 issued = true;
             }
             if (issued) {  // every MMA has retired before TMEM is freed
@@ -448,8 +478,10 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     } else if (epilogue) {
         // ------------------------------------------------ epilogue
         if (kMode == kDown) pdl_wait();  // Y, parts and tickets are other kernels' too until then
-        const int quad = warp & 3, c0 = (warp >> 2) * 32;  // channels c0 .. c0 + 31 of the tile
-        const int row = quad * 32 + lane;
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane, c0 = (warp >> 2) * 32;  // !kBoxA: a row, channels c0 .. c0 + 31 of the tile
+        const int ch = quad * 32 + lane;                          // kBoxA: a channel, all rows
+        constexpr int kPairs = kBoxA ? kNT / 2 : 16;              // sums, in pairs of channels (kBoxA: of rows)
         int buf = 0, slot = 0, stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -458,25 +490,41 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         for (int left = nu; left > 0; ++tile, kb = 0) {
             const int seg = min(kbt - kb, left);  // this share's units of the tile
             const bool starts = kb == 0, whole = seg == kbt;
-            uint64_t v[kA][16];  // pairs of channels c0 + 2 i, + 1
+            uint64_t v[kA][kPairs];
 #pragma unroll
             for (int a = 0; a < kA; ++a)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[a][i] = 0;
+                for (int i = 0; i < kPairs; ++i) v[a][i] = 0;
             for (int i = 0; i < seg; ++i) {
                 // after a wait that ran out the loops go on without waiting, so
                 // that every barrier and ticket below is still met
                 if (ok) ok = __all_sync(0xffffffffu, wait_fast(&done[stage], phase, wctx));
                 tc_fence_after();
-                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kA * 128 + c0);
+                const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kA * kCols + (kBoxA ? 0 : c0));
 #pragma unroll
                 for (int a = 0; a < kA; ++a) {
-                    const float s1 = slots[(slot * kA + a) * kNT + row];
-                    uint32_t r[32];
-                    tmem_ld32(t + (uint32_t)(a * 128), r);
-                    tmem_wait_ld32(r);
-                    fma32(v[a], r, f32x2(s1, s1));
-                    if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
+                    if constexpr (!kBoxA) {
+                        const float s1 = slots[(slot * kA + a) * kNT + row];
+                        uint32_t r[32];
+                        tmem_ld32(t + (uint32_t)(a * kCols), r);
+                        tmem_wait_ld32(r);
+                        fma32(v[a], r, f32x2(s1, s1));
+                        if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
+                    } else {
+                        const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(slots + (slot * kA + a) * kNT);
+                        if constexpr (kNT == 32) {
+                            uint32_t r[32];
+                            tmem_ld32(t + (uint32_t)(a * kCols), r);
+                            tmem_wait_ld32(r);
+                            fma_scaled<8>(v[a], r, s2);
+                            if (kA == 2) pin16(v[a]);
+                        } else {
+                            uint32_t r[16];
+                            tmem_ld16(t + (uint32_t)(a * kCols), r);
+                            tmem_wait_ld16(r);
+                            fma_scaled<4>(v[a], r, s2);
+                        }
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -491,22 +539,31 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             left -= seg;
 
             const int m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
-            const bool in = m0 + row < p.M;
+            const bool in = m0 + row < p.M;  // (!kBoxA)
             if (!whole || kMode == kGateUp) {
                 // this CTA's sums of the tile, [rows][kA][128 channels]; slot 0 for a tile that
                 // began in an earlier share, slot 1 for one that begins here and goes on,
                 // slots 2 and 3 for whole ones
                 const int ps = !whole ? (starts ? 1 : 0) : 2 + (whole_tiles & 1);
                 if (kMode == kGateUp && whole && whole_tiles >= 2) named_bar_sync(4 + (whole_tiles & 1), kEpiThreads + 32 * kFin);
-                if (in) {
-                    float4* part = reinterpret_cast<float4*>(p.parts + (size_t)(kSlotsCta * c + ps) * slot_floats +
-                                                             (size_t)row * (kA * 128) + c0);
+                float* const part = p.parts + (size_t)(kSlotsCta * c + ps) * slot_floats;
+                if constexpr (kBoxA) {
+#pragma unroll
+                    for (int a = 0; a < kA; ++a)
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i) {
+                            const float2 x = f32x2_parts(v[a][i]);
+                            if (2 * i < p.part_rows) __stcg(part + (2 * i * kA + a) * 128 + ch, x.x);
+                            if (2 * i + 1 < p.part_rows) __stcg(part + ((2 * i + 1) * kA + a) * 128 + ch, x.y);
+                        }
+                } else if (in) {
+                    float4* to = reinterpret_cast<float4*>(part + (size_t)row * (kA * 128) + c0);
 #pragma unroll
                     for (int a = 0; a < kA; ++a)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float2 x = f32x2_parts(v[a][2 * i]), y = f32x2_parts(v[a][2 * i + 1]);
-                            __stcg(part + a * 32 + i, make_float4(x.x, x.y, y.x, y.y));
+                            __stcg(to + a * 32 + i, make_float4(x.x, x.y, y.x, y.y));
                         }
                 }
                 if (kMode == kGateUp && whole) {
@@ -515,8 +572,18 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 }
                 continue;
             }
-            const int n = (kMode == kRows ? tile / p.MB : tile) * 128 + c0;
-            if (in) {
+            const int n = (kMode == kRows ? tile / p.MB : tile) * 128 + (kBoxA ? ch : c0);
+            if constexpr (kBoxA) {
+                if (n < p.N) {
+                    uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + n;  // (kNT rows hold all: m0 is 0)
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        const float2 f = f32x2_parts(v[0][i]);
+                        if (2 * i < p.M) y[(size_t)(2 * i) * p.N] = T::from_float(f.x);
+                        if (2 * i + 1 < p.M) y[(size_t)(2 * i + 1) * p.N] = T::from_float(f.y);
+                    }
+                }
+            } else if (in) {
                 uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -568,7 +635,8 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         settle();
         if (kMode == kDown) pdl_wait();
         // unless kFuse: scales of the rows and of the boxes, and routing weights, of the unit at kb
-        float ax[kQ], ar[kQ], aw = 0.0f, aw2 = 0.0f;
+        constexpr int kPer = (kNT + 31) / 32;  // rows per lane
+        float ax[kPer], ar[kPer], aw = 0.0f, aw2 = 0.0f;
         int we = -1;  // kDown: the expert that ar is of
         const auto load = [&]() {
             const float* xs = p.xs + kb * p.xs_pitch + mb * kNT;
@@ -580,7 +648,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 if (e != we) {
                     we = e;
 #pragma unroll
-                    for (int j = 0; j < kQ; ++j) {
+                    for (int j = 0; j < kPer; ++j) {
                         const int m = lane + 32 * j;
                         ar[j] = 0.0f;  // the token's weight for this expert
                         if (m < p.M)
@@ -592,27 +660,27 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             aw = __ldg(p.ws + o);
             if (kA == 2) aw2 = __ldg(p.ws2 + o);
 #pragma unroll
-            for (int j = 0; j < kQ; ++j) {
+            for (int j = 0; j < kPer; ++j) {
                 const int m = lane + 32 * j;
                 ax[j] = mb * kNT + m < p.M ? xs[m] : 0.0f;
             }
         };
 #pragma unroll
-        for (int j = 0; j < kQ; ++j) ax[j] = 0.0f, ar[j] = 1.0f;
+        for (int j = 0; j < kPer; ++j) ax[j] = 0.0f, ar[j] = 1.0f;
         if (!kFuse && sidx < kSide && sidx < nu) load();
         for (int i = sidx < kSide ? sidx : nu; i < nu; i += kSide) {
             const int stage = i % kStages, slot = i % kSlots;
             const uint32_t phase = (uint32_t)(i / kStages) & 1u;
             float* s = slots + slot * (kA * kNT);
             if constexpr (kFuse) {
-                static_assert(kMode == kRows && kNT == 32, "fused codes: the plain product of at most 32 rows");
+                static_assert(kMode == kRows && kBoxA, "fused codes: the plain product of at most 32 rows");
                 // 8 lanes per row, 16 values each; 4 rows per step
                 const int chunk = lane & 7, rsub = lane >> 3;
                 const int k = kb * 128 + chunk * 16;
                 const int steps = (p.M + 3) >> 2;
-                uint4 x[8][2];
+                uint4 x[kNT / 4][2];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < kNT / 4; ++r) {
                     if (r < steps) {
                         const int m = r * 4 + rsub;
                         x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
@@ -627,7 +695,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 if (!__all_sync(0xffffffffu, wait_fast(&done[stage], phase ^ 1, wctx))) break;
                 uint8_t* sx = xring + stage * (kNT * 128);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < kNT / 4; ++r) {
                     if (r < steps) {
                         const int m = r * 4 + rsub;
                         float a = T::pair_max(fp8_amax8<T>(fp8_amax8<T>(T::as_pair(0u), x[r][0]), x[r][1]));
@@ -642,15 +710,16 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 }
                 fence_proxy_async_smem();
             } else {
-                float f[kQ], g[kQ];  // this unit's products; the next one's are loaded meanwhile
+                float f[kPer], g[kPer];  // this unit's products; the next one's are loaded meanwhile
 #pragma unroll
-                for (int j = 0; j < kQ; ++j) f[j] = __fmul_rn(ax[j], aw * ar[j]), g[j] = __fmul_rn(ax[j], aw2);
+                for (int j = 0; j < kPer; ++j) f[j] = __fmul_rn(ax[j], aw * ar[j]), g[j] = __fmul_rn(ax[j], aw2);
                 kb += kSide;
                 settle();
                 if (i + kSide < nu) load();
                 if (!__all_sync(0xffffffffu, wait_fast(&done[stage], phase ^ 1, wctx))) break;
 #pragma unroll
-                for (int j = 0; j < kQ; ++j) {
+                for (int j = 0; j < kPer; ++j) {
+                    if (kNT == 16 && lane >= 16) break;
                     s[lane + 32 * j] = f[j];
                     if (kA == 2) s[kNT + lane + 32 * j] = g[j];
                 }
@@ -685,7 +754,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         }
         named_bar_sync(1, 32 * kJoinWarps);
         const int f = *last_flag;
-        const int jw = epilogue ? (warp >> 2) * kQ + (warp & 3) : 4 * kQ + role - 2;  // 0 .. kJoinWarps - 1
+        const int jw = !epilogue ? kEpiWarps + role - 2 : kBoxA ? warp : (warp >> 2) * kQ + (warp & 3);  // 0 .. kJoinWarps - 1
         if (f) {
             // one tile: a row per warp; two: half of the warps each
             const bool both = f == 3;
@@ -702,7 +771,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     __syncthreads();
     if (role == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, 512);
+        tmem_dealloc(tmem_base, kTmemCols);
     }
 }
 
