@@ -137,7 +137,7 @@ cudaError_t launch_quant_fp8(const uint16_t* X, int dtype, int M, int K, uint8_t
                              long long sb, int sms, cudaStream_t s) {
     const int KB = cdiv(K, 128);
     const long long nblocks = (long long)M * KB;
-    const long long per = (long long)(kQuantThreads / 16) * kQuantBlocks;
+    const long long per = (long long)(kQuantThreads / 8) * kQuantBlocks;
     const int grid = (int)std::max<long long>(1, std::min<long long>((nblocks + per - 1) / per, (long long)sms * 16));
     return dtype == INT8MM_F16
                ? launch(k_quant_fp8<F16>, dim3(grid), dim3(kQuantThreads), 0, s, true, X, nblocks, K, KB, codes, scales,
@@ -399,7 +399,7 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     r.tickets = reinterpret_cast<unsigned*>(b + L.tickets);
     r.xq = b + L.xq;
     r.xs = reinterpret_cast<float*>(b + L.xs);
-    const dim3 rgrid(r.log_blocks + cdiv((long long)T * HB, kRouteThreads / 16));
+    const dim3 rgrid(r.log_blocks + cdiv((long long)T * HB, kRouteThreads / 8));
     cudaError_t e;
 #define I8_ROUTE(TT) \
     (f16 ? launch(k_moe_route<TT, F16>, rgrid, dim3(kRouteThreads), 0, s, true, r) \

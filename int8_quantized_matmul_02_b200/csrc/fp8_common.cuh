@@ -27,6 +27,17 @@ __device__ __forceinline__ float fp8_block_scale(float amax) {
     return fmaxf(__fdiv_rn(amax, kE4m3Max), kFp8ScaleFloor);
 }
 
+// The same for a maximum of 16-bit values, without the division: q = a * c with
+// c = RN(1 / 448), then one correction by the exact remainder (Markstein's
+// division with a fused multiply-add).  Equal to RN(a / 448) for every fp16
+// and bf16 value that reaches the floor (tested for each of them).
+__device__ __forceinline__ float fp8_block_scale16(float amax) {
+    constexpr float c = 1.0f / kE4m3Max;
+    const float q = __fmul_rn(amax, c);
+    const float s = __fmaf_rn(__fmaf_rn(-kE4m3Max, q, amax), c, q);
+    return amax > 3.4e38f ? amax : fmaxf(s, kFp8ScaleFloor);  // an infinite maximum stays infinite
+}
+
 // Two codes in 16 bits: lo in bits 0-7, hi in bits 8-15.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;

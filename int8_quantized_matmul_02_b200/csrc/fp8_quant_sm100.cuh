@@ -2,56 +2,69 @@
 // consecutive k) and of weights (one scale per 128 x 128 block); the rule is
 // in fp8_common.cuh.
 //
-// Activations: bound by HBM, 2 bytes read and 1 written per value.  A block of
-// 128 16-bit values is 16 lanes x 16 bytes, so a half-warp holds it in
-// registers, takes its maximum with packed 16-bit instructions and four
-// shuffles, and writes 8 codes per lane.  A warp reads 512 consecutive bytes;
-// each half-warp has kQuantBlocks blocks in flight.
+// Activations: bound by HBM, 2 bytes read and 1 written per value, if the
+// instructions per value are few.  A block of 128 16-bit values is held by 8
+// lanes in registers, 8 values of either half of the block each (so that both
+// loads of a warp are whole lines); its maximum takes packed 16-bit
+// instructions and three shuffles, its scale no division, and where the next
+// block lies is found by additions.  kQuantBlocks blocks are in flight per
+// group of 8 lanes.
 #pragma once
 
 #include "fp8_common.cuh"
 
 namespace i8mm {
 
-constexpr int kQuantBlocks = 4;    // blocks of 128 in flight per half-warp
+constexpr int kQuantBlocks = 2;    // blocks of 128 in flight per group of 8 lanes
 constexpr int kQuantThreads = 256;
 
-// Half-warp `hw` of `nhw` takes blocks hw, hw + nhw, ... of the M x KB blocks
-// (row-major).  scale(m, b) goes to scales[m * sm + b * sb].
+// Group `gr` of `ngr` groups of 8 lanes takes blocks gr, gr + ngr, ... of the
+// M x KB blocks (row-major; ngr a multiple of 4).  scale(m, b) goes to
+// scales[m * sm + b * sb].
 template <typename T>
 __device__ __forceinline__ void quant_fp8_blocks(const uint16_t* __restrict__ X, long long nblocks, int K, int KB,
                                                  uint8_t* __restrict__ codes, float* __restrict__ scales, long long sm,
-                                                 long long sb, long long hw, long long nhw) {
-    const int sub = threadIdx.x & 15;  // this lane's 8 values of the block
-    // every half-warp of a warp runs the same number of rounds: the shuffles
-    // below stay inside a half-warp but name the whole warp
-    const long long first = hw - ((threadIdx.x >> 4) & 1);
-    for (long long w0 = first; w0 < nblocks; w0 += nhw * kQuantBlocks) {
-        const long long b0 = w0 + ((threadIdx.x >> 4) & 1);
-        uint4 x[kQuantBlocks];
-        long long m[kQuantBlocks];
-        int kb[kQuantBlocks];
-        bool in[kQuantBlocks];
+                                                 long long sb, long long gr, long long ngr) {
+    const int sub = threadIdx.x & 7;
+    const long long dm = ngr / KB;
+    const int dk = (int)(ngr - dm * KB);
+    long long m = gr / KB, b = gr;
+    int kb = (int)(gr - m * KB);
+    // every group of a warp runs the same number of rounds: the shuffles below
+    // stay inside a group but name the whole warp
+    for (long long w0 = gr - ((threadIdx.x >> 3) & 3); w0 < nblocks; w0 += ngr * kQuantBlocks) {
+        uint4 x[kQuantBlocks][2];
+        long long at[kQuantBlocks], sat[kQuantBlocks];
+        bool in[kQuantBlocks][2];
 #pragma unroll
         for (int i = 0; i < kQuantBlocks; ++i) {
-            const long long b = b0 + nhw * i;
-            m[i] = b < nblocks ? b / KB : 0;
-            kb[i] = b < nblocks ? (int)(b - m[i] * KB) : 0;
-            in[i] = b < nblocks && kb[i] * 128 + sub * 8 < K;  // K % 16 == 0: all 8 values or none
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (in[i]) x[i] = __ldg(reinterpret_cast<const uint4*>(X + m[i] * K + kb[i] * 128 + sub * 8));
+            const int k = kb * 128 + sub * 8;
+            at[i] = m * K + k;
+            sat[i] = m * sm + kb * sb;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                in[i][h] = b < nblocks && k + 64 * h < K;  // K % 16 == 0: all 8 values or none
+                x[i][h] = make_uint4(0, 0, 0, 0);
+                if (in[i][h]) x[i][h] = __ldg(reinterpret_cast<const uint4*>(X + at[i] + 64 * h));
+            }
+            b += ngr;
+            m += dm;
+            kb += dk;
+            if (kb >= KB) {
+                kb -= KB;
+                ++m;
+            }
         }
 #pragma unroll
         for (int i = 0; i < kQuantBlocks; ++i) {
-            float a = T::pair_max(fp8_amax8<T>(T::as_pair(0u), x[i]));
+            float a = T::pair_max(fp8_amax8<T>(fp8_amax8<T>(T::as_pair(0u), x[i][0]), x[i][1]));
 #pragma unroll
-            for (int d = 8; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-            const float s = fp8_block_scale(a);
-            if (in[i]) {
-                *reinterpret_cast<uint2*>(codes + m[i] * K + kb[i] * 128 + sub * 8) =
-                    fp8_codes8<T>(x[i], __frcp_rn(s));
-                if (sub == 0) scales[m[i] * sm + kb[i] * sb] = s;
-            }
+            for (int d = 4; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+            const float s = fp8_block_scale16(a), inv = __frcp_rn(s);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (in[i][h]) *reinterpret_cast<uint2*>(codes + at[i] + 64 * h) = fp8_codes8<T>(x[i][h], inv);
+            if (sub == 0 && in[i][0]) scales[sat[i]] = s;
         }
     }
 }
@@ -63,8 +76,8 @@ __global__ void __launch_bounds__(kQuantThreads)
                 float* __restrict__ scales, long long sm, long long sb) {
     pdl_wait();
     pdl_launch_dependents();
-    const long long hw = ((long long)blockIdx.x * kQuantThreads + threadIdx.x) >> 4;
-    quant_fp8_blocks<T>(X, nblocks, K, KB, codes, scales, sm, sb, hw, (long long)gridDim.x * (kQuantThreads / 16));
+    const long long gr = ((long long)blockIdx.x * kQuantThreads + threadIdx.x) >> 3;
+    quant_fp8_blocks<T>(X, nblocks, K, KB, codes, scales, sm, sb, gr, (long long)gridDim.x * (kQuantThreads / 8));
 }
 
 // One 128 x 128 block of a weight per thread block: W is K x N (row-major, 16

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         const int m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
         const int nb = kMode == kRows ? t / p.MB : kMode == kGateUp ? t % p.NB : t;
         const int n = nb * 128 + 4 * lane;
-        const int e = kMode == kGateUp ? __ldcg(p.active + 1 + t / p.NB) : 0;
+        [[maybe_unused]] const int e = kMode == kGateUp ? __ldcg(p.active + 1 + t / p.NB) : 0;
 #pragma unroll 1
         for (int r0 = row0; r0 < rows; r0 += step * kR) {
             float4 sum[kR][kA];
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         float a = T::pair_max(fp8_amax8<T>(fp8_amax8<T>(T::as_pair(0u), x[r][0]), x[r][1]));
 #pragma unroll
                         for (int d = 4; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                        const float sc = fp8_block_scale(a), inv = __frcp_rn(sc);
+                        const float sc = fp8_block_scale16(a), inv = __frcp_rn(sc);
                         const uint2 lo = fp8_codes8<T>(x[r][0], inv), hi = fp8_codes8<T>(x[r][1], inv);
                         *reinterpret_cast<uint4*>(sx + m * 128 + ((chunk ^ (m & 7)) << 4)) =
                             make_uint4(lo.x, lo.y, hi.x, hi.y);

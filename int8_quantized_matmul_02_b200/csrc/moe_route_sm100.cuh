@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(kRouteThreads)
     if ((int)blockIdx.x >= p.log_blocks) {
         const int KB = (p.H + 127) / 128;
         const long long b = (int)blockIdx.x - p.log_blocks, nb = (int)gridDim.x - p.log_blocks;
-        quant_fp8_blocks<T>(p.X, (long long)p.T * KB, p.H, KB, p.xq, p.xs, 1, p.T, (b * kRouteThreads + tid) >> 4,
-                            nb * (kRouteThreads / 16));
+        quant_fp8_blocks<T>(p.X, (long long)p.T * KB, p.H, KB, p.xq, p.xs, 1, p.T, (b * kRouteThreads + tid) >> 3,
+                            nb * (kRouteThreads / 8));
         return;
     }
     const int eb = (p.E + kRouteExperts - 1) / kRouteExperts;

@@ -63,6 +63,21 @@ def test_quantize_every_value(cuda_ok, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_scale_of_every_maximum(cuda_ok, dtype):
+    """Each finite value of the type as the maximum of a block, in the
+    quantiser (the product's kernel forms its scales by the same function)."""
+    v = torch.arange(0, 32768, dtype=torch.int32).to(torch.int16).view(dtype)
+    v = v[torch.isfinite(v.float())]
+    v = v[: v.numel() // 256 * 256].view(-1, 256)          # row: 256 blocks
+    X = torch.zeros(v.shape[0], 256, 128, dtype=dtype)
+    X[:, :, 77] = -v
+    X = X.view(v.shape[0], -1)
+    codes, scales = i8.quantize_fp8(X.cuda())
+    q, s = ref.quantize(_np(X))
+    assert np.array_equal(_np(scales), s) and _same_codes(codes, q)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_quantize_zero_tiny_and_large_blocks(cuda_ok, dtype):
     X = torch.zeros(6, 272, dtype=dtype)
     X[1, 5] = torch.finfo(dtype).smallest_normal
