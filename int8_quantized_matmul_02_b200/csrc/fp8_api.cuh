@@ -52,7 +52,7 @@ Fp8WsLayout fp8_ws_layout(int M, int K, int N) {
 }
 
 struct MoeWsLayout {
-    size_t status, logits, ids, wts, active, tickets, xq, xs, hq, hs, parts, total;
+    size_t status, logits, ids, wts, active, masks, tickets, xq, xs, hq, hs, parts, total;
     size_t t_gate, t_down;  // tickets of the two products, after the router's
 };
 
@@ -72,6 +72,7 @@ MoeWsLayout moe_ws_layout(int T, int H, int I, int E, int top_k) {
     L.ids = take((size_t)T * top_k * 4);
     L.wts = take((size_t)T * top_k * 4);
     L.active = take((size_t)(A + 1) * 4);
+    L.masks = take((size_t)A * 8);
     L.tickets = take((size_t)(T + 1) * 4);
     L.t_gate = take((size_t)A * cdiv(I, 128) * 4);
     L.t_down = take((size_t)cdiv(H, 128) * 4);
@@ -396,6 +397,7 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     r.ids = ids;
     r.wts = wts;
     r.active = reinterpret_cast<int32_t*>(b + L.active);
+    r.masks = reinterpret_cast<unsigned long long*>(b + L.masks);
     r.tickets = reinterpret_cast<unsigned*>(b + L.tickets);
     r.xq = b + L.xq;
     r.xs = reinterpret_cast<float*>(b + L.xs);
@@ -413,6 +415,7 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     p.MB = 1;
     p.active = r.active;
     p.max_active = A;
+    p.masks = r.masks;
     p.ids = ids;
     p.wts = wts;
     p.top_k = top_k;

@@ -47,7 +47,7 @@
 //   the first   is the TMA producer of the weight boxes (and of the rows
 //               unless kFuse);
 //   the second  allocates TMEM and issues the MMAs;
-//   the rest    (up to ten) take the units in turn: the unit's scale products
+//   the rest    (two to six) take the units in turn: the unit's scale products
 //               into shared memory, and with kFuse the rows' codes (the rows'
 //               16-bit values are read, quantised and written to the swizzled
 //               A operand).  In kGateUp two do that, and the others finish
@@ -77,6 +77,7 @@ struct Fp8RowsParams {
     const float* ws2;      // kGateUp: the up weight's
     const int32_t* active; // kGateUp, kDown: count, then the chosen experts in ascending order
     int max_active;        // the count is at most this
+    const unsigned long long* masks;  // for each chosen expert its tokens, a bit each
     const int32_t* ids;    // M x top_k chosen experts and their weights
     const float* wts;
     int top_k;
@@ -95,9 +96,10 @@ constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in join
 constexpr int kFRPrefetch = 10;  // boxes of the next product fetched into L2 per block (24 MB in all)
 constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
 
-// 16 epilogue warps leave no other below 16
+// 12 warps where the epilogue is 4 (168 registers a thread), 16 where it is 8
+// (128), 20 where it is 16 (96)
 template <int kNT>
-__host__ __device__ constexpr int fr_threads() { return kNT == 128 ? 640 : 512; }
+__host__ __device__ constexpr int fr_threads() { return kNT == 128 ? 640 : kNT == 64 ? 512 : 384; }
 template <int kMode>
 __host__ __device__ constexpr int fr_a() { return kMode == kGateUp ? 2 : 1; }
 template <int kNT>
@@ -106,8 +108,12 @@ template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_bufs() { return kNT <= 32 ? 4 : 512 / (128 * fr_a<kMode>()); }  // accumulators
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stage_bytes() { return fr_a<kMode>() * 16384 + kNT * 128; }
+// !kBoxA: a 32-row x 64-byte staging buffer per epilogue warp (rows 80 bytes apart)
+constexpr int kFRStageRow = 80;
+template <int kNT>
+__host__ __device__ constexpr int fr_out_bytes() { return kNT <= 32 ? 0 : 4 * (kNT / 32) * 32 * kFRStageRow; }
 template <int kMode, int kNT>
-__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + (fr_bufs<kMode, kNT>() + 1) * 8 + 64; }
+__host__ __device__ constexpr int fr_fixed_bytes() { return 1024 + fr_out_bytes<kNT>() + (fr_bufs<kMode, kNT>() + 1) * 8 + 64; }
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_bytes(int stages) {
     return fr_fixed_bytes<kMode, kNT>() + stages * (fr_stage_bytes<kMode, kNT>() + 16) +
@@ -164,11 +170,31 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
 }
 
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15])::"memory");
+// tmem_wait_ld32 / 16 with a look (that does not wait) at a barrier taken before
+// the wait: the answers arrive together.
+__device__ __forceinline__ bool tmem_wait_ld_look(uint32_t (&r)[32], uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%33], %34;\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "selp.u32 %32, 1, 0, p;\n\t}\n"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool tmem_wait_ld_look(uint32_t (&r)[16], uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%17], %18;\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "selp.u32 %16, 1, 0, p;\n\t}\n"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // v[0 .. 2 kQuads - 1] (4 kQuads sums) += r * s, a scale for each.
@@ -180,6 +206,28 @@ __device__ __forceinline__ void fma_scaled(uint64_t* v, const uint32_t* r, const
         fma_f32x2(v[2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
         fma_f32x2(v[2 * i + 1], f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
     }
+}
+
+// 64 bytes of each of 32 rows (a lane's w is its row's) to dst + row * stride,
+// through a staging buffer: written as they are, 16 bytes of 32 rows at a time,
+// they take 32 transactions a store (4500 cycles for a tile of 128 rows).
+// Rows from `rows` on, rows not in `mask` and 16-byte pieces from `pieces` on
+// are left out.
+__device__ __forceinline__ void store_rows64(uint8_t* stage, int lane, const uint32_t (&w)[16], uint8_t* dst, size_t stride,
+                                             int rows, int pieces, uint32_t mask) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(stage + lane * kFRStageRow + q * 16) =
+            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    __syncwarp();
+    const int piece = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = j * 8 + (lane >> 2);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * kFRStageRow + piece * 16);
+        if (r < rows && ((mask >> r) & 1u) && piece < pieces) __stcg(reinterpret_cast<uint4*>(dst + r * stride + piece * 16), x);
+    }
+    __syncwarp();
 }
 
 // Nothing that follows is moved before the computation of v, nor that after it.
@@ -226,7 +274,8 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     // those were issued after the epilogue had read the slot's last content
     // (an accumulator is released only once its scales have been read).
     float* slots = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // [slots][kA][kNT]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(slots + kSlots * kA * kNT);
+    uint8_t* outs = reinterpret_cast<uint8_t*>(slots + kSlots * kA * kNT);  // [epilogue warps][32 rows][80]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(outs + fr_out_bytes<kNT>());
     uint64_t* full = bars;                         // [stages] boxes, rows and scales are there
     uint64_t* done = bars + kStages;               // [stages] the stage's MMAs are complete
     uint64_t* tempty = bars + 2 * kStages;         // [bufs] the epilogue has read the accumulator
@@ -293,15 +342,16 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         const int m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
         const int nb = kMode == kRows ? t / p.MB : kMode == kGateUp ? t % p.NB : t;
         const int n = nb * 128 + 4 * lane;
-        [[maybe_unused]] const int e = kMode == kGateUp ? __ldcg(p.active + 1 + t / p.NB) : 0;
+        // kGateUp: rows that did not choose the expert have no sums; their codes are zero
+        const unsigned long long mask = kMode == kGateUp ? __ldcg(p.masks + t / p.NB) : ~0ull;
 #pragma unroll 1
         for (int r0 = row0; r0 < rows; r0 += step * kR) {
             float4 sum[kR][kA];
-            int id[kR];
+            bool have[kR];
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
                 const int row = r0 + r * step;
-                id[r] = kMode == kGateUp && row < rows && lane < p.top_k ? __ldcg(p.ids + row * p.top_k + lane) : -1;
+                have[r] = row < rows && (kMode != kGateUp || ((mask >> row) & 1u));
 #pragma unroll
                 for (int a = 0; a < kA; ++a) sum[r][a] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -316,7 +366,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         const int row = r0 + r * step;
 #pragma unroll
                         for (int a = 0; a < kA; ++a)
-                            x[o][r][a] = o0 + o <= cl && row < rows ? __ldcg(from + (row * kA + a) * 32)
+                            x[o][r][a] = o0 + o <= cl && have[r] ? __ldcg(from + (row * kA + a) * 32)
                                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 }
@@ -338,7 +388,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 if (row >= rows) continue;  // the same for the whole warp
                 if constexpr (kMode == kGateUp) {
                     const int a = t / p.NB;
-                    const bool chosen = __any_sync(0xffffffffu, id[r] == e);
+                    const bool chosen = have[r];
                     const float4 g = sum[r][0], up = sum[r][kA - 1];
                     float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (chosen)
@@ -481,15 +531,21 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         const int quad = warp & 3;
         const int row = quad * 32 + lane, c0 = (warp >> 2) * 32;  // !kBoxA: a row, channels c0 .. c0 + 31 of the tile
         const int ch = quad * 32 + lane;                          // kBoxA: a channel, all rows
+        uint8_t* const out = outs + ((warp >> 2) * kQ + quad) * (32 * kFRStageRow);
         constexpr int kPairs = kBoxA ? kNT / 2 : 16;              // sums, in pairs of channels (kBoxA: of rows)
         int buf = 0, slot = 0, stage = 0;
         uint32_t phase = 0;
-        bool ok = true;
+        bool ok = true, seen = false;  // the next unit's MMAs are known to be complete
         int whole_tiles = 0;
         int tile = first_tile, kb = first_kb;
         for (int left = nu; left > 0; ++tile, kb = 0) {
             const int seg = min(kbt - kb, left);  // this share's units of the tile
             const bool starts = kb == 0, whole = seg == kbt;
+            // kGateUp: the tokens that chose the tile's expert; the others' sums are not stored
+            // (the word with this warp's rows)
+            const uint32_t mask =
+                kMode == kGateUp ? __ldcg(reinterpret_cast<const uint32_t*>(p.masks + tile / p.NB) + (kBoxA ? 0 : quad))
+                                 : ~0u;
             uint64_t v[kA][kPairs];
 #pragma unroll
             for (int a = 0; a < kA; ++a)
@@ -498,8 +554,13 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             for (int i = 0; i < seg; ++i) {
                 // after a wait that ran out the loops go on without waiting, so
                 // that every barrier and ticket below is still met
-                if (ok) ok = __all_sync(0xffffffffu, wait_fast(&done[stage], phase, wctx));
+                if (ok && !__all_sync(0xffffffffu, seen))
+                    ok = __all_sync(0xffffffffu, wait_fast(&done[stage], phase, wctx));
                 tc_fence_after();
+                // (a look past the share's last unit is at a barrier of this block all the
+                // same, and its answer is not used)
+                const int next = stage + 1 == kStages ? 0 : stage + 1;
+                const uint32_t next_phase = stage + 1 == kStages ? phase ^ 1 : phase;
                 const uint32_t t = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * kA * kCols + (kBoxA ? 0 : c0));
 #pragma unroll
                 for (int a = 0; a < kA; ++a) {
@@ -507,7 +568,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         const float s1 = slots[(slot * kA + a) * kNT + row];
                         uint32_t r[32];
                         tmem_ld32(t + (uint32_t)(a * kCols), r);
-                        tmem_wait_ld32(r);
+                        seen = tmem_wait_ld_look(r, &done[next], next_phase);
                         fma32(v[a], r, f32x2(s1, s1));
                         if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
                     } else {
@@ -515,13 +576,13 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         if constexpr (kNT == 32) {
                             uint32_t r[32];
                             tmem_ld32(t + (uint32_t)(a * kCols), r);
-                            tmem_wait_ld32(r);
+                            seen = tmem_wait_ld_look(r, &done[next], next_phase);
                             fma_scaled<8>(v[a], r, s2);
                             if (kA == 2) pin16(v[a]);
                         } else {
                             uint32_t r[16];
                             tmem_ld16(t + (uint32_t)(a * kCols), r);
-                            tmem_wait_ld16(r);
+                            seen = tmem_wait_ld_look(r, &done[next], next_phase);
                             fma_scaled<4>(v[a], r, s2);
                         }
                     }
@@ -531,15 +592,12 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 if (lane == 0) mbar_arrive(&tempty[buf]);
                 if (++buf == kBufs) buf = 0;
                 if (++slot == kSlots) slot = 0;
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
+                stage = next;
+                phase = next_phase;
             }
             left -= seg;
 
             const int m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
-            const bool in = m0 + row < p.M;  // (!kBoxA)
             if (!whole || kMode == kGateUp) {
                 // this CTA's sums of the tile, [rows][kA][128 channels]; slot 0 for a tile that
                 // began in an earlier share, slot 1 for one that begins here and goes on,
@@ -553,17 +611,24 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
 #pragma unroll
                         for (int i = 0; i < kPairs; ++i) {
                             const float2 x = f32x2_parts(v[a][i]);
-                            if (2 * i < p.part_rows) __stcg(part + (2 * i * kA + a) * 128 + ch, x.x);
-                            if (2 * i + 1 < p.part_rows) __stcg(part + ((2 * i + 1) * kA + a) * 128 + ch, x.y);
+                            if (2 * i < p.part_rows && ((mask >> (2 * i)) & 1u)) __stcg(part + (2 * i * kA + a) * 128 + ch, x.x);
+                            if (2 * i + 1 < p.part_rows && ((mask >> (2 * i + 1)) & 1u)) __stcg(part + ((2 * i + 1) * kA + a) * 128 + ch, x.y);
                         }
-                } else if (in) {
-                    float4* to = reinterpret_cast<float4*>(part + (size_t)row * (kA * 128) + c0);
+                } else {
 #pragma unroll
                     for (int a = 0; a < kA; ++a)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 x = f32x2_parts(v[a][2 * i]), y = f32x2_parts(v[a][2 * i + 1]);
-                            __stcg(to + a * 32 + i, make_float4(x.x, x.y, y.x, y.y));
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 x = f32x2_parts(v[a][8 * q + i]);
+                                w[2 * i] = __float_as_uint(x.x);
+                                w[2 * i + 1] = __float_as_uint(x.y);
+                            }
+                            store_rows64(out, lane, w,
+                                         reinterpret_cast<uint8_t*>(part + (size_t)(quad * 32) * (kA * 128) + a * 128 + c0 + 16 * q),
+                                         kA * 128 * 4, p.M - m0 - quad * 32, 4, mask);
                         }
                 }
                 if (kMode == kGateUp && whole) {
@@ -583,19 +648,17 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         if (2 * i + 1 < p.M) y[(size_t)(2 * i + 1) * p.N] = T::from_float(f.y);
                     }
                 }
-            } else if (in) {
-                uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n;
+            } else {
+                uint32_t w[16];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = f32x2_parts(v[0][4 * q + i]);
-                        w[i] = T::pack(f.x, f.y);
-                    }
-                    if (n + q * 8 < p.N)  // N % 16 == 0
-                        *reinterpret_cast<uint4*>(y + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 16; ++i) {
+                    const float2 f = f32x2_parts(v[0][i]);
+                    w[i] = T::pack(f.x, f.y);
                 }
+                // N % 16 == 0: a 16-byte piece is in or out
+                store_rows64(out, lane, w,
+                             reinterpret_cast<uint8_t*>(reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + quad * 32) * p.N + n),
+                             (size_t)p.N * 2, p.M - m0 - quad * 32, (p.N - n) >> 3, ~0u);
             }
         }
     } else if (kFin > 0 && role >= 2 + kSide) {

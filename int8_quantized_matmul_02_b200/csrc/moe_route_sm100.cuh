@@ -26,6 +26,7 @@ struct RouteParams {
     int32_t* ids;            // T x top_k
     float* wts;              // T x top_k
     int32_t* active;         // count, then chosen experts
+    unsigned long long* masks;  // for each of those the tokens that chose it, a bit each
     unsigned* tickets;       // one per token group and one more, zero between calls
     uint8_t* xq;             // T x H codes, scales [b * T + t]
     float* xs;
@@ -47,7 +48,7 @@ template <int kTT, typename T>
 __global__ void __launch_bounds__(kRouteThreads)
     k_moe_route(const RouteParams p) {
     __shared__ double red[kRouteThreads / 32][kRouteExperts * kTT];
-    __shared__ int flags[kMaxExperts];
+    __shared__ unsigned chose[kMaxExperts][2];  // the tokens that chose an expert, a bit each
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kRouteThreads)
         if (last) p.tickets[tg] = 0;
         s_last = last;
     }
-    for (int e = tid; e < kMaxExperts; e += kRouteThreads) flags[e] = 0;
+    for (int e = tid; e < kMaxExperts; e += kRouteThreads) chose[e][0] = chose[e][1] = 0;
     __syncthreads();
     if (!s_last) return;
 
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kRouteThreads)
         if (lane < p.top_k) {
             __stcg(p.ids + (size_t)t * p.top_k + lane, mine_id);
             __stcg(p.wts + (size_t)t * p.top_k + lane, __fdiv_rn(mine, sum));
-            flags[mine_id] = 1;  // all there is to list if these are the only tokens
+            atomicOr(&chose[mine_id][t >> 5], 1u << (t & 31));  // all there is to list if these are the only tokens
         }
     }
     const int groups = (p.T + kTT - 1) / kTT;
@@ -195,14 +196,22 @@ __global__ void __launch_bounds__(kRouteThreads)
         }
         __syncthreads();
         if (!s_last) return;
-        for (int i = tid; i < p.T * p.top_k; i += kRouteThreads) flags[__ldcg(p.ids + i)] = 1;
+        for (int i = tid; i < p.T * p.top_k; i += kRouteThreads) {
+            const int t = i / p.top_k;
+            atomicOr(&chose[__ldcg(p.ids + i)][t >> 5], 1u << (t & 31));
+        }
     }
     __syncthreads();
     if (warp == 0) {
         int n = 0;
         for (int e = lane; e < kMaxExperts; e += 32) {
-            const unsigned m = __ballot_sync(0xffffffffu, flags[e] != 0);
-            if (flags[e]) p.active[1 + n + __popc(m & ((1u << lane) - 1u))] = e;
+            const unsigned lo = chose[e][0], hi = chose[e][1];
+            const unsigned m = __ballot_sync(0xffffffffu, (lo | hi) != 0);
+            if (lo | hi) {
+                const int at = n + __popc(m & ((1u << lane) - 1u));
+                p.active[1 + at] = e;
+                p.masks[at] = (unsigned long long)hi << 32 | lo;
+            }
             n += __popc(m);
         }
         if (lane == 0) p.active[0] = n;
