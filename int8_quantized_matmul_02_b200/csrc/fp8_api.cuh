@@ -154,8 +154,8 @@ cudaError_t launch_rows(int dev, int grid, const CUtensorMap& tw, const CUtensor
     static_assert(smem <= kMaxSmemOptin, "shared memory of one SM");
     cudaError_t e = fp8_opt_in<k_fp8_rows<kMode, kNT, kFuse, T>>(dev, smem);
     if (e != cudaSuccess) return e;
-    return launch(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kNT>()), smem, s, pdl, tw, tw2, tx,
-                  tnext, p);
+    return launch_ex(k_fp8_rows<kMode, kNT, kFuse, T>, dim3(grid), dim3(fr_threads<kNT>()), smem, s, pdl,
+                     p.cut > 1 ? p.cut : 0, tw, tw2, tx, tnext, p);
 }
 
 template <int kBN, typename T>
@@ -185,11 +185,32 @@ bool fp8_opts(const int8mm_forward_opts* o, Fp8Opts* out) {
     return (out->ev0 == nullptr) == (out->ev1 == nullptr);
 }
 
-// Whether the weight-streaming kernel takes a product of M rows.
+// Into how many pieces the weight-streaming kernel cuts each of `tiles` tiles
+// for a cluster of as many blocks (1: a tile per block), or 0 for equal runs
+// of units that are joined through memory.
+//   - Up to 32 rows the stored sums are small: clusters only where they fill
+//     the device as well as the runs do.
+//   - More rows: a cluster as large as there are idle SMs for, so long as a
+//     piece keeps kFRMinUnits units.  For 128 x 4096 x 11008 (86 tiles)
+//     uncut, runs take 26.2 us; for 100 x 11008 x 4096 (32 tiles) 24.0 us.
+//     More tiles than SMs: runs.
+int fp8_cut(DeviceInfo* info, int tiles, int units_per_tile, int nt, int ctas) {
+    if (tiles > ctas) return 0;
+    int c = std::min({8, ctas / tiles, std::max(1, units_per_tile / kFRMinUnits)});
+    while (c > 1 && c * tiles > cluster_capacity(info, c) * c) --c;
+    if (nt <= 32) {
+        const int most = std::max(tiles, std::min(ctas, tiles * units_per_tile / kFRMinUnits));
+        return c > 1 && 5 * c * tiles >= 4 * most ? c : 0;
+    }
+    return c;
+}
+
+// Whether the weight-streaming kernel takes a product of M rows: up to 128 rows
+// each weight box is read once (100 x 11008 x 4096: 24 us against 46 us tiled);
+// above, as long as its 128 x 128 tiles are one wave (512 x 4096 x 4096: 20.5
+// against 22.8 us; 256 x 4096 x 11008, two waves: 33.4 against 23.3 us).
 bool fp8_rows_path(int M, int N, int sms) {
-    (void)N;
-    (void)sms;
-    return M <= 128;
+    return M <= 128 || (M <= kFp8RowsMaxM && (long long)cdiv(M, 128) * cdiv(N, 128) <= sms);
 }
 
 }  // namespace
@@ -300,7 +321,8 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 128)) return INT8MM_ERR_CUDA;
         tb = ta;  // unused when the codes are made in the kernel
         if (!fuse && !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, (uint32_t)nt)) return INT8MM_ERR_CUDA;
-        const int grid = FrShares(p.NB * p.MB, KB, sms).count;
+        p.cut = fp8_cut(info, p.NB * p.MB, KB, nt, sms);
+        const int grid = FrShares(p.NB * p.MB, KB, sms, p.cut).count;
         if (timed) e = cudaEventRecord(o.ev0, s);
         if (e != cudaSuccess) return cuda_status(e);
         const bool pdl = !timed;
@@ -438,6 +460,9 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     g.tickets = reinterpret_cast<unsigned*>(b + L.t_gate);
     // (how many experts the tokens reach is known on the device only: blocks past the shares leave)
     const int ggrid = std::min(ctas, std::max(A * IB, A * IB * HB / kFRMinUnits));
+    // (the chosen experts are at least top_k)
+    g.next_cut = fp8_cut(info, HB, top_k * IB, nt, ctas);
+    g.next_grid = g.next_cut ? g.next_cut * HB : std::min(ctas, std::max(HB, A * IB * HB / kFRMinUnits));
     e = nt == 16   ? launch_rows<kGateUp, 16, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
         : nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
                    : launch_rows<kGateUp, 64, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true);
@@ -453,7 +478,8 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     d.Y = Y;
     d.test_flags = 0;
     d.tickets = reinterpret_cast<unsigned*>(b + L.t_down);
-    const int dgrid = std::min(ctas, std::max(HB, A * IB * HB / kFRMinUnits));
+    d.cut = g.next_cut;
+    const int dgrid = g.next_grid;
 #define I8_DOWN(NT)                                                                        \
     (f16 ? launch_rows<kDown, NT, false, F16>(dev, dgrid, td, td, th, td, d, s, true)          \
          : launch_rows<kDown, NT, false, BF16>(dev, dgrid, td, td, th, td, d, s, true))

@@ -29,6 +29,11 @@
 // to come adds the stored sums in the order of k: the result does not depend
 // on who that is, and no CTA waits for another.
 //
+// With many rows that join costs more than it spreads (8 us for 128 rows: one
+// block reads all the others' sums).  There, a tile is cut for the blocks of a
+// cluster, which leave their sums in shared memory and each finish a part of
+// the rows, reading from one another; or it is not cut at all.
+//
 // Three products are made of this:
 //   kRows    Y = X W;
 //   kGateUp  per chosen expert h = silu(X Wg) * (X Wu), two boxes per unit, h
@@ -84,6 +89,8 @@ struct Fp8RowsParams {
     void* Y;               // kRows, kDown: M x N, 16 bits
     uint8_t* hq;           // kGateUp: codes [a][M][N], scales [(a * NB + nb) * M + m]
     float* hs;
+    int cut;               // blocks of a cluster that share each tile (1: a tile per block); 0: FrShares' own choice
+    int next_grid, next_cut;  // kGateUp: grid and cut of the down product
     float* parts;          // per CTA two slots (kGateUp: four) of part_rows x kA x 128 floats
     int part_rows;         // rows of a tile: min(M, kNT)
     unsigned* tickets;     // one per tile, zero between calls
@@ -110,6 +117,7 @@ template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_stage_bytes() { return fr_a<kMode>() * 16384 + kNT * 128; }
 // !kBoxA: a 32-row x 64-byte staging buffer per epilogue warp (rows 80 bytes apart)
 constexpr int kFRStageRow = 80;
+constexpr int kFRSumRow = 132;  // floats from row to row of a tile's sums in shared memory
 template <int kNT>
 __host__ __device__ constexpr int fr_out_bytes() { return kNT <= 32 ? 0 : 4 * (kNT / 32) * 32 * kFRStageRow; }
 template <int kMode, int kNT>
@@ -138,8 +146,13 @@ __host__ __device__ constexpr int fr_smem_bytes() { return fr_bytes<kMode, kNT>(
 // (Units are 16 KB of weight each, so their number is far below 2^31.)
 struct FrShares {
     int kbt, count, cut, per, more;
-    __host__ __device__ __forceinline__ FrShares(int tiles, int kbt_, int ctas) : kbt(kbt_), cut(0) {
+    __host__ __device__ __forceinline__ FrShares(int tiles, int kbt_, int ctas, int cut_ = 0) : kbt(kbt_), cut(cut_) {
         const int units = tiles * kbt;
+        if (cut) {
+            count = cut * tiles;
+            per = more = 0;
+            return;
+        }
         int most = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
         if (most > ctas) most = ctas;
         const int c = tiles < most ? most / tiles : 0;
@@ -208,6 +221,19 @@ __device__ __forceinline__ void fma_scaled(uint64_t* v, const uint32_t* r, const
     }
 }
 
+// 16 bytes of the shared memory of CTA `rank` of the cluster, at this CTA's address `addr`.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}\n"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // 64 bytes of each of 32 rows (a lane's w is its row's) to dst + row * stride,
 // through a staging buffer: written as they are, 16 bytes of 32 rows at a time,
 // they take 32 transactions a store (4500 cycles for a tile of 128 rows).
@@ -265,6 +291,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     // a side warp waits for the stage's last completion by parity, so it must not be two rounds
     // ahead: its previous unit, kSide earlier, has seen that unit's stage done one round earlier
     static_assert(kSide <= kStages, "side warps");
+    static_assert(kNT * kFRSumRow * 4 <= kStages * kStageBytes, "a tile's sums fit the ring");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* xring = smem;                         // [stages][kNT rows]; reads of M = 128 rows run on into wring
@@ -328,7 +355,8 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     const int kbt = kMode == kDown ? p.KB * n_active : p.KB;  // units per tile
     const int tiles = kMode == kRows ? p.NB * p.MB : kMode == kGateUp ? p.NB * n_active : p.NB;
     const int c = (int)blockIdx.x;
-    const FrShares sh(tiles, kbt, (int)gridDim.x);
+    const FrShares sh(tiles, kbt, (int)gridDim.x, p.cut);
+    const bool clustered = kMode != kGateUp && p.cut > 1;
     const int C = sh.count;
     const int nu = c < C ? sh.start(c + 1) - sh.start(c) : 0;  // this CTA's units
     const int first_tile = sh.start(c) / kbt, first_kb = sh.start(c) - first_tile * kbt;
@@ -481,7 +509,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 // the down product's first boxes of this block's share, into L2 while the
                 // last tiles are joined and the next kernel starts
                 const int kbd = p.NB * n_active;
-                const FrShares sd(p.KB, kbd, (int)gridDim.x);
+                const FrShares sd(p.KB, kbd, p.next_grid, p.next_cut);
                 if (c < sd.count) {
                     const int end = min(sd.start(c + 1), sd.start(c) + kFRPrefetch);
                     for (int u = sd.start(c); u < end; ++u) {
@@ -598,13 +626,32 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             left -= seg;
 
             const int m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
-            if (!whole || kMode == kGateUp) {
+            if (!whole || kMode == kGateUp || clustered) {
                 // this CTA's sums of the tile, [rows][kA][128 channels]; slot 0 for a tile that
                 // began in an earlier share, slot 1 for one that begins here and goes on,
                 // slots 2 and 3 for whole ones
                 const int ps = !whole ? (starts ? 1 : 0) : 2 + (whole_tiles & 1);
                 if (kMode == kGateUp && whole && whole_tiles >= 2) named_bar_sync(4 + (whole_tiles & 1), kEpiThreads + 32 * kFin);
                 float* const part = p.parts + (size_t)(kSlotsCta * c + ps) * slot_floats;
+                if (clustered) {
+                    // every box and row of this share has been read: the ring holds the sums now
+                    float* mine = reinterpret_cast<float*>(smem);
+                    if constexpr (kBoxA) {
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i) {
+                            const float2 x = f32x2_parts(v[0][i]);
+                            mine[(2 * i) * kFRSumRow + ch] = x.x;
+                            mine[(2 * i + 1) * kFRSumRow + ch] = x.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 x = f32x2_parts(v[0][2 * i]), y = f32x2_parts(v[0][2 * i + 1]);
+                            *reinterpret_cast<float4*>(mine + row * kFRSumRow + c0 + 4 * i) = make_float4(x.x, x.y, y.x, y.y);
+                        }
+                    }
+                    continue;
+                }
                 if constexpr (kBoxA) {
 #pragma unroll
                     for (int a = 0; a < kA; ++a)
@@ -798,11 +845,35 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
 
     // The tiles that this share holds only a part of come last, after it has
     // been streamed: the sums are stored by now, and nothing waits for this.
+    if (clustered) {
+        __syncwarp();
+        cluster_sync_all();  // everyone's sums are in shared memory
+        const int t = c / p.cut, m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
+        const int n = (kMode == kRows ? t / p.MB : t) * 128 + 4 * lane;
+        constexpr int kWarps = fr_threads<kNT>() / 32;
+        const uint32_t at = smem_u32(smem) + (uint32_t)lane * 16;
+#pragma unroll 1
+        for (int row = (int)cluster_ctarank() * kWarps + warp; row < rows; row += p.cut * kWarps) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int o = 0; o < p.cut; ++o) {  // in the order of k
+                const float4 x = ld_cluster_v4(at + (uint32_t)row * (kFRSumRow * 4), (uint32_t)o);
+                sum.x = __fadd_rn(sum.x, x.x);
+                sum.y = __fadd_rn(sum.y, x.y);
+                sum.z = __fadd_rn(sum.z, x.z);
+                sum.w = __fadd_rn(sum.w, x.w);
+            }
+            if (n < p.N)  // N % 16 == 0
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n) =
+                    make_uint2(T::pack(sum.x, sum.y), T::pack(sum.z, sum.w));
+        }
+        cluster_sync_all();  // nobody leaves while its sums are read
+    }
     const int end_kb = first_kb + nu;  // the share's end, in units from its first tile's start
     const int head_tile = nu > 0 && first_kb > 0 ? first_tile : -1;
     const int tail_tile =
         nu > 0 && end_kb % kbt != 0 && (first_kb == 0 || end_kb > kbt) ? first_tile + end_kb / kbt : -1;
-    if (role != 0 && role != 1 && (head_tile >= 0 || tail_tile >= 0)) {
+    if (!clustered && role != 0 && role != 1 && (head_tile >= 0 || tail_tile >= 0)) {
         named_bar_sync(1, 32 * kJoinWarps);
         if (warp == 0) {  // lane 0: the head's ticket, lane 1: the tail's
             const int t = lane == 0 ? head_tile : lane == 1 ? tail_tile : -1;
