@@ -15,7 +15,6 @@ attention-projection layers of a transformer.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import numpy as np
@@ -395,18 +394,18 @@ def forward_grouped(X: torch.Tensor, w: GroupedWeight, threshold: float = 6.0, *
 _DTYPES = {torch.float16: _abi.F16, torch.bfloat16: _abi.BF16}
 
 
-_NO_SWITCH = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream  # of a device, as the integer that the C interface takes
 
 
 def _on(device: torch.device, stream=None):
     """A context with `device` current, and `stream` if given, so that what a
     call allocates belongs to the stream that it launches on."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _same_device(what: str, device: torch.device, *tensors) -> None:
@@ -415,8 +414,8 @@ def _same_device(what: str, device: torch.device, *tensors) -> None:
             raise ValueError(f"{what} must be on one device")
 
 
-def _check_out(t: torch.Tensor | None, name: str, shape, dtype: torch.dtype, device: torch.device) -> None:
-    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+def _check_out(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: torch.device) -> None:
+    if (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
@@ -429,17 +428,21 @@ def quantize_fp8(X: torch.Tensor, codes: torch.Tensor | None = None, scales: tor
     if not (X.is_cuda and X.dtype in _DTYPES and X.dim() == 2 and X.is_contiguous()):
         raise ValueError("X must be a contiguous 2-D float16 or bfloat16 CUDA tensor")
     dev = X.device
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return quantize_fp8(X, codes, scales)
     M, K = X.shape
     kb = (K + 127) // 128
-    _check_out(codes, "codes", (M, K), torch.float8_e4m3fn, dev)
-    _check_out(scales, "scales", (M, kb), torch.float32, dev)
-    with _on(dev, stream):
-        if codes is None:
-            codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
-        if scales is None:
-            scales = torch.empty((M, kb), dtype=torch.float32, device=dev)
-        st = _abi.load().int8mm_quantize_fp8(X.data_ptr(), _DTYPES[X.dtype], M, K, codes.data_ptr(), scales.data_ptr(),
-                                             _current_stream(dev.index))
+    if codes is None:
+        codes = torch.empty_like(X, dtype=torch.float8_e4m3fn)
+    else:
+        _check_out(codes, "codes", (M, K), torch.float8_e4m3fn, dev)
+    if scales is None:
+        scales = X.new_empty(M, kb, dtype=torch.float32)
+    else:
+        _check_out(scales, "scales", (M, kb), torch.float32, dev)
+    st = _abi.load().int8mm_quantize_fp8(X.data_ptr(), _DTYPES[X.dtype], M, K, codes.data_ptr(), scales.data_ptr(),
+                                         _current_stream(dev.index))
     if st:
         _abi.check(st, "int8mm_quantize_fp8")
     return codes, scales
@@ -530,21 +533,25 @@ def forward_fp8(X: torch.Tensor, w: Fp8Weight, *, out: torch.Tensor | None = Non
     dev = w.device
     if X.dtype not in _DTYPES or X.dim() != 2 or X.shape[1] != w.K or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous float16 or bfloat16 tensor of shape (M, {w.K}) on {dev}")
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return forward_fp8(X, w, out=out, workspace=workspace, path=path, wait_limit_ns=wait_limit_ns,
+                               test_flags=test_flags)
     M = X.shape[0]
-    if workspace is not None and ((workspace.M, workspace.K, workspace.N) != (M, w.K, w.N)
-                                  or workspace.buf.device != dev):
+    if workspace is None:
+        workspace = Fp8Workspace(M, w.K, w.N, device=dev)
+    elif (workspace.M, workspace.K, workspace.N) != (M, w.K, w.N) or workspace.buf.device != dev:
         raise ValueError("workspace was made for another shape or device")
-    _check_out(out, "out", (M, w.N), X.dtype, dev)
-    with _on(dev, stream):
-        if workspace is None:
-            workspace = Fp8Workspace(M, w.K, w.N, device=dev)
-        Y = out if out is not None else X.new_empty(M, w.N)
-        st = _abi.load().int8mm_forward_fp8(X.data_ptr(), _DTYPES[X.dtype], M, w.ref, Y.data_ptr(),
-                                            workspace.buf.data_ptr(), workspace.nbytes,
-                                            _fp8_opts(path, wait_limit_ns, test_flags), _current_stream(dev.index))
+    if out is None:
+        out = X.new_empty(M, w.N)
+    else:
+        _check_out(out, "out", (M, w.N), X.dtype, dev)
+    st = _abi.load().int8mm_forward_fp8(X.data_ptr(), _DTYPES[X.dtype], M, w.ref, out.data_ptr(),
+                                        workspace.buf.data_ptr(), workspace.nbytes,
+                                        _fp8_opts(path, wait_limit_ns, test_flags), _current_stream(dev.index))
     if st:
         _abi.check(st, "int8mm_forward_fp8")
-    return Y
+    return out
 
 
 # ---------------------------------------------------------------------------- mixture of experts
@@ -624,25 +631,29 @@ def forward_moe_fp8(X: torch.Tensor, w: MoeFp8Weight, top_k: int, *, renormalize
     dev = w.device
     if X.dtype != w.router.dtype or X.dim() != 2 or X.shape[1] != w.H or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous {w.router.dtype} tensor of shape (T, {w.H}) on {dev}")
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return forward_moe_fp8(X, w, top_k, renormalize=renormalize, out=out, workspace=workspace,
+                                   return_routing=return_routing, wait_limit_ns=wait_limit_ns, test_flags=test_flags)
     T = X.shape[0]
-    if workspace is not None and (
-            (workspace.T, workspace.H, workspace.I, workspace.E, workspace.top_k) != (T, w.H, w.I, w.E, top_k)
-            or workspace.buf.device != dev):
+    if workspace is None:
+        workspace = MoeWorkspace(T, w, top_k)
+    elif ((workspace.T, workspace.H, workspace.I, workspace.E, workspace.top_k) != (T, w.H, w.I, w.E, top_k)
+          or workspace.buf.device != dev):
         raise ValueError("workspace was made for another shape or device")
-    _check_out(out, "out", (T, w.H), X.dtype, dev)
+    if out is None:
+        out = X.new_empty(T, w.H)
+    else:
+        _check_out(out, "out", (T, w.H), X.dtype, dev)
     ids = wts = None
-    with _on(dev, stream):
-        if workspace is None:
-            workspace = MoeWorkspace(T, w, top_k)
-        Y = out if out is not None else X.new_empty(T, w.H)
-        if return_routing:
-            ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-            wts = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        st = _abi.load().int8mm_forward_moe_fp8(
-            X.data_ptr(), _DTYPES[X.dtype], T, w.ref, top_k, int(bool(renormalize)), Y.data_ptr(),
-            ids.data_ptr() if return_routing else None, wts.data_ptr() if return_routing else None,
-            workspace.buf.data_ptr(), workspace.nbytes, _fp8_opts("auto", wait_limit_ns, test_flags),
-            _current_stream(dev.index))
+    if return_routing:
+        ids = X.new_empty(T, top_k, dtype=torch.int32)
+        wts = X.new_empty(T, top_k, dtype=torch.float32)
+    st = _abi.load().int8mm_forward_moe_fp8(
+        X.data_ptr(), _DTYPES[X.dtype], T, w.ref, top_k, int(bool(renormalize)), out.data_ptr(),
+        ids.data_ptr() if return_routing else None, wts.data_ptr() if return_routing else None,
+        workspace.buf.data_ptr(), workspace.nbytes, _fp8_opts("auto", wait_limit_ns, test_flags),
+        _current_stream(dev.index))
     if st:
         _abi.check(st, "int8mm_forward_moe_fp8")
-    return (Y, ids, wts) if return_routing else Y
+    return (out, ids, wts) if return_routing else out
