@@ -381,7 +381,8 @@ int8mm_status int8mm_noalloc_device_status(void* stream, int32_t* n_outliers);
 enum { INT8MM_F16 = 0, INT8MM_BF16 = 1 };
 
 /* codes (device, M x K e4m3) and scales (device, M x ceil(K/128) fp32) of X
- * (device, M x K, 16 bits).  Allocates nothing and needs no workspace. */
+ * (device, M x K, 16 bits); the three must not overlap.  Allocates nothing and
+ * needs no workspace. */
 int8mm_status int8mm_quantize_fp8(const uint16_t* X, int dtype, int M, int K, uint8_t* codes, float* scales,
                                   void* stream);
 
@@ -411,7 +412,7 @@ size_t int8mm_fp8_workspace_bytes(int M, int K, int N);
  *   Y[m,n] = 16-bit( sum_b xs[m,b] * ws[n/128,b] * sum_{k in block b} xq[m,k] wq[n,k] ),
  * with X's codes and scales formed by the call; the sums of a block are the
  * tensor cores' fp32 sums, the sum over blocks is fp32.  The result does not
- * depend on what else runs.
+ * depend on what else runs.  X and Y must not overlap.
  * opts may be NULL.  path: INT8MM_PATH_AUTO, _GEMM (tiled, SM pairs) or
  * _DECODE (weight-streaming, M <= 1024); acc_out must be NULL; events, wait
  * limit and test flags as for int8mm_forward_ex. */
@@ -450,8 +451,9 @@ size_t int8mm_moe_workspace_bytes(int T, int H, int I, int E, int top_k);
  *   Y = 16-bit( sum over the token's experts of weight * (h Wd) ), fp32 sums.
  * topk_ids (device, T x top_k int32, best first) and topk_weights (device,
  * T x top_k fp32) receive the routing; each may be NULL.  Only the weights of
- * chosen experts are read.  opts may be NULL; path and events must be unset.
- */
+ * chosen experts are read, and an infinity or a NaN in an expert's weights
+ * reaches the tokens that chose it and no other.  Y may be X.  opts may be
+ * NULL; path and events must be unset. */
 int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const int8mm_moe_weight* w, int top_k,
                                      int renormalize, uint16_t* Y, int32_t* topk_ids, float* topk_weights, void* ws,
                                      size_t ws_bytes, const int8mm_forward_opts* opts, void* stream);

@@ -7,6 +7,11 @@ constexpr int kFp8RowsMaxM = 1024;  // rows the weight-streaming kernel takes (i
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxTopK = 16;
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 bool dtype_ok(int dtype) { return dtype == INT8MM_F16 || dtype == INT8MM_BF16; }
 
 // Rows per tile of the weight-streaming kernel for M rows.
@@ -221,6 +226,10 @@ int8mm_status int8mm_quantize_fp8(const uint16_t* X, int dtype, int M, int K, ui
                                   void* stream) {
     if (!X || !codes || !scales || !dtype_ok(dtype) || !shape_ok(M, K, 16)) return INT8MM_ERR_INVALID_ARGUMENT;
     if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return INT8MM_ERR_MISALIGNED;
+    const size_t values = (size_t)M * K, blocks = (size_t)M * cdiv(K, 128);
+    if (overlap(X, 2 * values, codes, values) || overlap(X, 2 * values, scales, 4 * blocks) ||
+        overlap(codes, values, scales, 4 * blocks))
+        return INT8MM_ERR_INVALID_ARGUMENT;
     int dev;
     DeviceInfo* info;
     int8mm_status st = current_device(&dev, &info);
@@ -282,6 +291,8 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         return INT8MM_ERR_MISALIGNED;
     const Fp8WsLayout L = fp8_ws_layout(M, K, N);
     if (ws_bytes < L.total) return INT8MM_ERR_WORKSPACE_TOO_SMALL;
+    // up to 32 rows are quantised by the blocks that multiply them, beside others' stores to Y
+    if (overlap(X, (size_t)M * K * 2, Y, (size_t)M * N * 2)) return INT8MM_ERR_INVALID_ARGUMENT;
     int dev;
     DeviceInfo* info;
     int8mm_status st = current_device(&dev, &info);

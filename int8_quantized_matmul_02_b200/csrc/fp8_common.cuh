@@ -149,25 +149,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// One 128-byte K block: D[tmem] = A[smem] * B[smem]^T, four e4m3 MMAs of
-// K = 32 (32 bytes = +2 in the descriptors' address field apart), the first
-// one overwriting D.
-__device__ __forceinline__ void mma_e4m3_k128(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-    const uint32_t z = 0, one = 1;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%4, %4, %4, %4}, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, {%4, %4, %4, %4}, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, {%4, %4, %4, %4}, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, {%4, %4, %4, %4}, q;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(z), "r"(one)
-        : "memory");
-}
-
 // A unit of the weight-streaming kernel in one block: a look at the two
 // barriers that the next unit needs, this unit's MMAs, and a commit to `done`
 // unless !commit.  kA boxes of one operand (16 KB apart: the A operand if
@@ -222,7 +203,9 @@ __device__ __forceinline__ uint32_t mma_unit(uint32_t d_tmem, uint64_t a_desc, u
 }
 #undef I8MM_MMA4
 
-// mma_e4m3_k128 on an SM pair (issued by the even CTA's elected thread).
+// One 128-byte K block on an SM pair (issued by the even CTA's elected thread):
+// D[tmem] = A[smem] * B[smem]^T, four e4m3 MMAs of K = 32 (32 bytes = +2 in the
+// descriptors' address field apart), the first one overwriting D.
 __device__ __forceinline__ void mma_e4m3_k128_2sm(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
     const uint32_t z = 0, one = 1;
     asm volatile(

@@ -43,8 +43,10 @@
 //            are one product over the concatenated k of the chosen experts,
 //            with the routing weight in the scale, so the weighted sum of a
 //            token's experts happens in the same running sums.
-// In the gated layer every token is a row for every expert; tokens that did
-// not choose an expert have zero codes and scales there.
+// In the gated layer every token is a row for every expert.  Of tokens that did
+// not choose an expert kGateUp stores zero codes, and kDown leaves out what the
+// accumulators hold for them there (kFRNotChosen): an infinity or a NaN
+// in an expert's weights reaches the tokens that chose it and no other.
 //
 // Warps: the epilogue is warps 0-3 (a TMEM lane quadrant of channels each) for
 // kNT <= 32; above, with rows in kQ quadrants, the warps w with w % 4 < kQ
@@ -101,6 +103,9 @@ struct Fp8RowsParams {
 
 constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
 constexpr int kFRPrefetch = 10;  // boxes of the next product fetched into L2 per block (24 MB in all)
+// in place of the scale of a row that did not choose the expert (-FLT_MAX: no
+// product of scales is that, whatever a caller's weight scales are)
+constexpr float kFRNotChosen = -3.40282347e38f;
 constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
 
 // 12 warps where the epilogue is 4 (168 registers a thread), 16 where it is 8
@@ -210,14 +215,25 @@ __device__ __forceinline__ bool tmem_wait_ld_look(uint32_t (&r)[16], uint64_t* b
     return ok != 0;
 }
 
-// v[0 .. 2 kQuads - 1] (4 kQuads sums) += r * s, a scale for each.
-template <int kQuads>
+// v[0 .. 2 kQuads - 1] (4 kQuads sums) += r * s, a scale for each; with kSkip a
+// sum whose scale is kFRNotChosen stays as it is, whatever r holds (r counts as 0).
+template <int kQuads, bool kSkip>
 __device__ __forceinline__ void fma_scaled(uint64_t* v, const uint32_t* r, const ulonglong2* s) {
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
         const ulonglong2 f = s[i];
-        fma_f32x2(v[2 * i], f32x2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), f.x);
-        fma_f32x2(v[2 * i + 1], f32x2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), f.y);
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(r[4 * i + j]);
+        if constexpr (kSkip) {
+            const float2 lo = f32x2_parts(f.x), hi = f32x2_parts(f.y);
+            x[0] = lo.x == kFRNotChosen ? 0.0f : x[0];
+            x[1] = lo.y == kFRNotChosen ? 0.0f : x[1];
+            x[2] = hi.x == kFRNotChosen ? 0.0f : x[2];
+            x[3] = hi.y == kFRNotChosen ? 0.0f : x[3];
+        }
+        fma_f32x2(v[2 * i], f32x2(x[0], x[1]), f.x);
+        fma_f32x2(v[2 * i + 1], f32x2(x[2], x[3]), f.y);
     }
 }
 
@@ -597,7 +613,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         uint32_t r[32];
                         tmem_ld32(t + (uint32_t)(a * kCols), r);
                         seen = tmem_wait_ld_look(r, &done[next], next_phase);
-                        fma32(v[a], r, f32x2(s1, s1));
+                        if (kMode != kDown || s1 != kFRNotChosen) fma32(v[a], r, f32x2(s1, s1));
                         if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
                     } else {
                         const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(slots + (slot * kA + a) * kNT);
@@ -605,13 +621,13 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                             uint32_t r[32];
                             tmem_ld32(t + (uint32_t)(a * kCols), r);
                             seen = tmem_wait_ld_look(r, &done[next], next_phase);
-                            fma_scaled<8>(v[a], r, s2);
+                            fma_scaled<8, kMode == kDown>(v[a], r, s2);
                             if (kA == 2) pin16(v[a]);
                         } else {
                             uint32_t r[16];
                             tmem_ld16(t + (uint32_t)(a * kCols), r);
                             seen = tmem_wait_ld_look(r, &done[next], next_phase);
-                            fma_scaled<4>(v[a], r, s2);
+                            fma_scaled<4, kMode == kDown>(v[a], r, s2);
                         }
                     }
                 }
@@ -760,7 +776,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
 #pragma unroll
                     for (int j = 0; j < kPer; ++j) {
                         const int m = lane + 32 * j;
-                        ar[j] = 0.0f;  // the token's weight for this expert
+                        ar[j] = kFRNotChosen;  // the token's weight for this expert
                         if (m < p.M)
                             for (int q = 0; q < p.top_k; ++q)
                                 if (__ldcg(p.ids + m * p.top_k + q) == e) ar[j] = __ldcg(p.wts + m * p.top_k + q);
@@ -822,7 +838,10 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             } else {
                 float f[kPer], g[kPer];  // this unit's products; the next one's are loaded meanwhile
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) f[j] = __fmul_rn(ax[j], aw * ar[j]), g[j] = __fmul_rn(ax[j], aw2);
+                for (int j = 0; j < kPer; ++j) {
+                    f[j] = kMode == kDown && ar[j] == kFRNotChosen ? kFRNotChosen : __fmul_rn(ax[j], aw * ar[j]);
+                    g[j] = __fmul_rn(ax[j], aw2);
+                }
                 kb += kSide;
                 settle();
                 if (i + kSide < nu) load();

@@ -66,6 +66,19 @@ def test_forward_refusals(lib):
         assert _fwd(lib, M=M, nbytes=need - 1) == 3
 
 
+def test_overlapping_buffers_are_refused(lib):
+    """Up to 32 rows are quantised while other blocks store results, so Y may not
+    lie on X; nor may codes or scales lie on X or on one another."""
+    assert _quant(lib, codes=FAKE) == 1 and _quant(lib, codes=FAKE + 2032) == 1  # X: 4 x 256 values, 2048 bytes
+    assert _quant(lib, codes=FAKE + 4096, scales=FAKE + 2044) == 1
+    assert _quant(lib, codes=FAKE + 4096, scales=FAKE + 4096 + 1020) == 1
+    for M in (8, 40, 300):
+        w = _weight(256, 256)
+        assert _fwd(lib, M=M, w=w, Y=FAKE) == 1
+        assert _fwd(lib, M=M, w=w, Y=FAKE + M * 512 - 16) == 1
+        assert _fwd(lib, M=M, w=w, X=FAKE + M * 512 - 16) == 1
+
+
 def test_prepare_refusals(lib):
     out = _abi.Fp8Weight()
     need = lib.int8mm_fp8_weight_bytes(256, 384)

@@ -56,6 +56,10 @@ def _check(got, X, w, top_k, renorm):
     (17, 5, 3, 256, 640),      # 32 columns
     (33, 33, 4, 128, 128),     # 64 columns, an expert in a second group of 32
     (64, 12, 4, 400, 400),
+    # more than three whole tiles per block, so that its slots of sums are used again
+    (2, 256, 16, 128, 2064),
+    (24, 64, 8, 144, 1040),
+    (50, 80, 3, 128, 1040),
 ])
 def test_layer(cuda_ok, T, E, top_k, H, I, dtype, renorm):
     X, w = _case(T, E, H, I, dtype, T + E + H + I)
@@ -100,6 +104,32 @@ def test_tokens_that_are_not_finite_stay_alone(cuda_ok, T):
     assert ((ids2 >= 0) & (ids2 < 8)).all()
     y, err, _, _ = _want(X[keep], w, 2, True)
     ref.check(Y[keep], y, ref.out_bound(y, err, torch.bfloat16))
+
+
+@pytest.mark.parametrize("which", ["gate", "down", "down scales"])
+@pytest.mark.parametrize("T", [4, 20, 50])
+def test_weights_that_are_not_finite_reach_their_own_tokens_only(cuda_ok, T, which):
+    X, w = _case(T, 8, 272, 256, torch.bfloat16, 10)
+    X[:, 0], w.router[:, 0] = 0, 0
+    X[0, 0], w.router[5, 0] = 64, 64      # the first token chooses expert 5
+    clean, ids, _ = i8.forward_moe_fp8(X.cuda(), w, 2, return_routing=True)
+    chose = (ids == 5).any(1)
+    assert chose[0] and not chose.all()
+    if which == "down scales":
+        w.down[1][5] = float("inf")
+    else:
+        codes = (w.gate if which == "gate" else w.down)[0]
+        codes.view(torch.uint8)[5, ::3] = 0x7F      # the NaN code
+    Y = i8.forward_moe_fp8(X.cuda(), w, 2)
+    assert torch.equal(Y[~chose], clean[~chose])
+    assert not torch.isfinite(Y[chose]).all(1).any()
+
+
+def test_output_in_place_of_the_tokens(cuda_ok):
+    X, w = _case(7, 8, 272, 256, torch.float16, 11)
+    Xd = X.cuda()
+    want = i8.forward_moe_fp8(Xd, w, 3)
+    assert torch.equal(i8.forward_moe_fp8(Xd, w, 3, out=Xd), want)
 
 
 def test_another_stream_and_a_captured_call(cuda_ok):
