@@ -12,6 +12,14 @@ attention-projection layers of a transformer.
     w  = prepare_weight(W_fp16_KxN, keep_idx)      # once, at load
     ws = Workspace(M, K, N)                         # reusable scratch
     Y  = forward(X_fp16_MxK, w, threshold=6.0, workspace=ws)
+
+The same layers with block-scaled e4m3 codes (fp16 or bf16 tensors), and a
+mixture-of-experts layer of them for a few tokens:
+
+    w8 = prepare_weight_fp8(W_KxN)                  # or weight_fp8(codes, scales)
+    Y  = forward_fp8(X_MxK, w8, workspace=Fp8Workspace(M, K, N))
+    m  = prepare_moe_weight_fp8(router, gate, up, down)
+    Y  = forward_moe_fp8(X_TxH, m, top_k, workspace=MoeWorkspace(T, m, top_k))
 """
 from __future__ import annotations
 

@@ -30,7 +30,7 @@ Fp8Layout fp8_weight_layout(int K, int N) {
 }
 
 // Rows of the scales of X in the workspace (a block's scales are contiguous):
-// whole tiles of the tiled kernel, which reads four rows at a time and past M.
+// whole tiles of the tiled kernel, which reads the scales of rows past M too.
 long long fp8_pitch(int M) { return ((long long)M + 255) / 256 * 256; }
 
 struct Fp8WsLayout {
@@ -192,26 +192,45 @@ bool fp8_opts(const int8mm_forward_opts* o, Fp8Opts* out) {
 
 // Into how many pieces the weight-streaming kernel cuts each of `tiles` tiles
 // for a cluster of as many blocks (1: a tile per block), or 0 for equal runs
-// of units that are joined through memory.
-//   - Up to 32 rows the stored sums are small: clusters only where they fill
-//     the device as well as the runs do.
+// of units that are joined through memory.  A tile has `units` units, at least
+// `least` of them (they differ where the device decides on the experts).
+//   - Up to 32 rows: the shortest by this estimate (ns).  A block takes 240 per
+//     unit (up to 16 rows; 390 up to 32) or HBM 2.56, whichever is longer in
+//     all; a join through memory takes 2000 (4000) and 200 for each block that
+//     shares the tile, one in a cluster 900.
+//     Measured, 8 rows, runs against this choice: 4096 x 11008 13.7 -> 12.6 us
+//     (not cut), 8192 x 1024 11.4 -> 7.2 (8 pieces), 16384 x 2048 14.4 -> 11.8
+//     (6), 1024 x 14336 8.4 -> 6.4 (not cut); 16384 x 9728 stays with runs
+//     (32.0, not cut 33.1).
 //   - More rows: a cluster as large as there are idle SMs for, so long as a
 //     piece keeps kFRMinUnits units.  For 128 x 4096 x 11008 (86 tiles)
 //     uncut, runs take 26.2 us; for 100 x 11008 x 4096 (32 tiles) 24.0 us.
 //     More tiles than SMs: runs.
-int fp8_cut(DeviceInfo* info, int tiles, int units_per_tile, int nt, int ctas) {
+int fp8_cut(DeviceInfo* info, int tiles, int units, int least, int nt, int ctas) {
     if (tiles > ctas) return 0;
-    int c = std::min({8, ctas / tiles, std::max(1, units_per_tile / kFRMinUnits)});
-    while (c > 1 && c * tiles > cluster_capacity(info, c) * c) --c;
-    if (nt <= 32) {
-        const int most = std::max(tiles, std::min(ctas, tiles * units_per_tile / kFRMinUnits));
-        return c > 1 && 5 * c * tiles >= 4 * most ? c : 0;
+    const int most = std::min(8, ctas / tiles);
+    const auto fits = [&](int c) { return c == 1 || c * tiles <= cluster_capacity(info, c) * c; };
+    if (nt > 32) {
+        int c = std::min(most, std::max(1, least / kFRMinUnits));
+        while (!fits(c)) --c;
+        return c;
     }
-    return c;
+    const double unit = nt == 16 ? 240 : 390, hbm = 2.56 * tiles * units;
+    double best = std::max(unit * tiles * units / ctas, hbm) + (nt == 16 ? 2000 : 4000) +
+                  200.0 * ctas / tiles;
+    int cut = 0;
+    for (int c = 1; c <= most && (c == 1 || 2 * c <= least); ++c) {
+        const double t = std::max(unit * cdiv(units, c), hbm) + (c > 1 ? 900 : 0);
+        if (t <= best && fits(c)) {
+            best = t;
+            cut = c;
+        }
+    }
+    return cut;
 }
 
 // Whether the weight-streaming kernel takes a product of M rows: up to 128 rows
-// each weight box is read once (100 x 11008 x 4096: 24 us against 46 us tiled);
+// each weight box is read once (100 x 11008 x 4096: 19 us against 46 us tiled);
 // above, as long as its 128 x 128 tiles are one wave (512 x 4096 x 4096: 20.5
 // against 22.8 us; 256 x 4096 x 11008, two waves: 33.4 against 23.3 us).
 bool fp8_rows_path(int M, int N, int sms) {
@@ -332,7 +351,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 128)) return INT8MM_ERR_CUDA;
         tb = ta;  // unused when the codes are made in the kernel
         if (!fuse && !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, (uint32_t)nt)) return INT8MM_ERR_CUDA;
-        p.cut = fp8_cut(info, p.NB * p.MB, KB, nt, sms);
+        p.cut = fp8_cut(info, p.NB * p.MB, KB, KB, nt, sms);
         const int grid = FrShares(p.NB * p.MB, KB, sms, p.cut).count;
         if (timed) e = cudaEventRecord(o.ev0, s);
         if (e != cudaSuccess) return cuda_status(e);
@@ -472,7 +491,10 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     // (how many experts the tokens reach is known on the device only: blocks past the shares leave)
     const int ggrid = std::min(ctas, std::max(A * IB, A * IB * HB / kFRMinUnits));
     // (the chosen experts are at least top_k)
-    g.next_cut = fp8_cut(info, HB, top_k * IB, nt, ctas);
+    g.next_cut = fp8_cut(info, HB, A * IB, top_k * IB, nt, ctas);
+    // (few clusters that leave SMs idle lose against runs here: 16 tokens, 8 of 64 experts,
+    // 2048 x 1408, 6 pieces of 16 tiles 95.1 us, runs 90.6)
+    if (nt <= 32 && 5 * g.next_cut * HB < 4 * ctas) g.next_cut = 0;
     g.next_grid = g.next_cut ? g.next_cut * HB : std::min(ctas, std::max(HB, A * IB * HB / kFRMinUnits));
     e = nt == 16   ? launch_rows<kGateUp, 16, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
         : nt == 32 ? launch_rows<kGateUp, 32, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)
