@@ -194,34 +194,28 @@ bool fp8_opts(const int8mm_forward_opts* o, Fp8Opts* out) {
 // for a cluster of as many blocks (1: a tile per block), or 0 for equal runs
 // of units that are joined through memory.  A tile has `units` units, at least
 // `least` of them (they differ where the device decides on the experts).
-//   - Up to 32 rows: the shortest by this estimate (ns).  A block takes 240 per
-//     unit (up to 16 rows; 390 up to 32) or HBM 2.56, whichever is longer in
-//     all; a join through memory takes 2000 (4000) and 200 for each block that
-//     shares the tile, one in a cluster 900.
-//     Measured, 8 rows, runs against this choice: 4096 x 11008 13.7 -> 12.6 us
-//     (not cut), 8192 x 1024 11.4 -> 7.2 (8 pieces), 16384 x 2048 14.4 -> 11.8
-//     (6), 1024 x 14336 8.4 -> 6.4 (not cut); 16384 x 9728 stays with runs
-//     (32.0, not cut 33.1).
-//   - More rows: a cluster as large as there are idle SMs for, so long as a
-//     piece keeps kFRMinUnits units.  For 128 x 4096 x 11008 (86 tiles)
-//     uncut, runs take 26.2 us; for 100 x 11008 x 4096 (32 tiles) 24.0 us.
-//     More tiles than SMs: runs.
+// More tiles than SMs: runs.  Else the shortest by an estimate, whose figures
+// are fits to K = 512 .. 16384, N = 1024 .. 18432 with 8, 24, 48 and 100 rows;
+// there its choice was within 4 % of the best one.  Runs against this choice:
+// 8 rows, 4096 x 11008 13.7 -> 12.6 us (not cut), 8192 x 1024 11.4 -> 7.1 (8
+// pieces), 1024 x 14336 8.4 -> 6.4 (not cut); 100 rows, 4096 x 11008 23.0 ->
+// 18.5 (not cut), 11008 x 4096 24.0 -> 18.9 (4 pieces), but 16384 x 9728 stays
+// with runs (41.6, not cut 54.3).
 int fp8_cut(DeviceInfo* info, int tiles, int units, int least, int nt, int ctas) {
     if (tiles > ctas) return 0;
+    // ns: a unit in one block; a join through memory, and more of it for each
+    // block that shares the tile; a join in a cluster
+    static constexpr struct {
+        double unit, join, share, cluster;
+    } kCost[4] = {{240, 2000, 200, 900}, {200, 2000, 200, 700}, {275, 4300, 370, 1900}, {370, 9000, 700, 2000}};
+    const auto& k = kCost[nt == 16 ? 0 : nt == 32 ? 1 : nt == 64 ? 2 : 3];
+    const double hbm = 2.5 * tiles * units;  // every unit from HBM
     const int most = std::min(8, ctas / tiles);
-    const auto fits = [&](int c) { return c == 1 || c * tiles <= cluster_capacity(info, c) * c; };
-    if (nt > 32) {
-        int c = std::min(most, std::max(1, least / kFRMinUnits));
-        while (!fits(c)) --c;
-        return c;
-    }
-    const double unit = nt == 16 ? 240 : 390, hbm = 2.56 * tiles * units;
-    double best = std::max(unit * tiles * units / ctas, hbm) + (nt == 16 ? 2000 : 4000) +
-                  200.0 * ctas / tiles;
+    double best = std::max(k.unit * tiles * units / ctas, hbm) + k.join + k.share * ctas / tiles;
     int cut = 0;
     for (int c = 1; c <= most && (c == 1 || 2 * c <= least); ++c) {
-        const double t = std::max(unit * cdiv(units, c), hbm) + (c > 1 ? 900 : 0);
-        if (t <= best && fits(c)) {
+        const double t = std::max(k.unit * cdiv(units, c), hbm) + (c > 1 ? k.cluster : 0);
+        if (t <= best && (c == 1 || c * tiles <= cluster_capacity(info, c) * c)) {
             best = t;
             cut = c;
         }
@@ -310,7 +304,7 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         return INT8MM_ERR_MISALIGNED;
     const Fp8WsLayout L = fp8_ws_layout(M, K, N);
     if (ws_bytes < L.total) return INT8MM_ERR_WORKSPACE_TOO_SMALL;
-    // up to 32 rows are quantised by the blocks that multiply them, beside others' stores to Y
+    // up to 16 rows are quantised by the blocks that multiply them, beside others' stores to Y
     if (overlap(X, (size_t)M * K * 2, Y, (size_t)M * N * 2)) return INT8MM_ERR_INVALID_ARGUMENT;
     int dev;
     DeviceInfo* info;
@@ -324,7 +318,9 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
     const bool f16 = dtype == INT8MM_F16, timed = o.ev0 != nullptr;
     const bool rows = o.path == INT8MM_PATH_DECODE || (o.path == INT8MM_PATH_AUTO && fp8_rows_path(M, N, sms));
     const int nt = fp8_rows_nt(M);
-    const bool fuse = rows && nt <= 32;
+    // up to 16 rows each block quantises them again and a launch is saved (16 x 4096 x 4096: 8.0
+    // us against 9.0); more keep the side warps too busy (32 x 4096 x 11008: 20.2 against 15.5)
+    const bool fuse = rows && nt <= 16;
     cudaError_t e = cudaSuccess;
     if (!fuse) e = launch_quant_fp8(X, dtype, M, K, xq, xs, 1, fp8_pitch(M), info->sm_count, s);
     if (e != cudaSuccess) return cuda_status(e);
@@ -352,14 +348,15 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
         tb = ta;  // unused when the codes are made in the kernel
         if (!fuse && !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, (uint32_t)nt)) return INT8MM_ERR_CUDA;
         p.cut = fp8_cut(info, p.NB * p.MB, KB, KB, nt, sms);
-        const int grid = FrShares(p.NB * p.MB, KB, sms, p.cut).count;
+        p.shares = FrShares(p.NB * p.MB, KB, sms, p.cut);
+        const int grid = p.shares.count;
         if (timed) e = cudaEventRecord(o.ev0, s);
         if (e != cudaSuccess) return cuda_status(e);
         const bool pdl = !timed;
 #define I8_ROWS(NT, FUSE)                                                                           \
     (f16 ? launch_rows<kRows, NT, FUSE, F16>(dev, grid, ta, ta, tb, ta, p, s, pdl)                  \
          : launch_rows<kRows, NT, FUSE, BF16>(dev, grid, ta, ta, tb, ta, p, s, pdl))
-        e = nt == 16 ? I8_ROWS(16, true) : nt == 32 ? I8_ROWS(32, true) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
+        e = nt == 16 ? I8_ROWS(16, true) : nt == 32 ? I8_ROWS(32, false) : nt == 64 ? I8_ROWS(64, false) : I8_ROWS(128, false);
 #undef I8_ROWS
     } else {
         constexpr int bn = 256;

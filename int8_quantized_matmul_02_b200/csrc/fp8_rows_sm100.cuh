@@ -21,18 +21,19 @@
 //     scales of 64 or 128 rows, read by every thread, slowed the tensor core's
 //     own reads of shared memory to 2400 cycles a unit, against 260.)
 //
-// The units, ordered by output tile and then k, are cut into equal consecutive
-// shares, one per CTA (one CTA per SM), whatever the shape: a CTA's share may
-// start and end inside a tile.  Of a tile that several CTAs share every one
+// Where there are fewer tiles than SMs a block takes a tile, or a cluster's
+// blocks take equal pieces of one; the caller decides (`cut`).  Otherwise the
+// units, ordered by output tile and then k, are cut into equal consecutive
+// shares, one per CTA (one CTA per SM): a CTA's share may start and end inside
+// a tile.  Of a tile that several CTAs share every one
 // stores its fp32 sums; at the end of its share, so that the stream is never
 // held up, each takes a ticket for its first and last tile, and the last one
 // to come adds the stored sums in the order of k: the result does not depend
 // on who that is, and no CTA waits for another.
 //
-// With many rows that join costs more than it spreads (8 us for 128 rows: one
-// block reads all the others' sums).  There, a tile is cut for the blocks of a
-// cluster, which leave their sums in shared memory and each finish a part of
-// the rows, reading from one another; or it is not cut at all.
+// That join takes 2 us for 8 rows and 9 for 128 (one block reads all the
+// others' sums).  The blocks of a cluster leave their sums in shared memory and
+// each finish a part of the rows, reading from one another: 1 to 2 us.
 //
 // Three products are made of this:
 //   kRows    Y = X W;
@@ -63,9 +64,10 @@
 // At the end all but the first two join the shared tiles, a warp per row.
 //
 // Measured (calls back to back, weights from HBM): 1 x 12288 x 49152 95 us, 6.36
-// TB/s, which is what HBM gives; 8 x 4096 x 11008 13.6 us, of which 7 are the
-// stream and the rest the start, the first boxes' latency and the join;
-// 100 x 11008 x 4096 19 us and 333 x 4112 x 5136 21 us, bound by shared memory
+// TB/s, which is what HBM gives; 8 x 4096 x 11008 12.0 us, of which 9 are the
+// stream of 86 blocks (56 to 60 GB/s each) and the rest the start and the first
+// boxes' latency; 16 x 256 x 384 3.8 us, all start;
+// 100 x 11008 x 4096 18.5 us and 333 x 4112 x 5136 20.6 us, bound by shared memory
 // (a unit of 128 rows writes and reads 32 KB each way, 512 cycles at 128 bytes
 // a cycle, and takes ~670).  The gate/up kernel streams at 6.2 to 7 TB/s.
 #pragma once
@@ -76,6 +78,76 @@
 namespace i8mm {
 
 enum { kRows = 0, kGateUp = 1, kDown = 2 };
+
+constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
+constexpr int kFRPrefetch = 10;  // boxes of the next product fetched into L2 per block (24 MB in all)
+// in place of the scale of a row that did not choose the expert (-FLT_MAX: no
+// product of scales is that, whatever a caller's weight scales are)
+constexpr float kFRNotChosen = -3.40282347e38f;
+constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
+
+// How `tiles` tiles of kbt units are shared out on at most `ctas` CTAs: `cut`
+// pieces a tile if the caller says so, and where that keeps at least 4 of 5
+// CTAs busy (one SM's stream, 56 GB/s of a matrix that is not in L2, times 118
+// is still all that HBM gives).  Otherwise equal runs of units, of `per` units
+// each, the first `more` of them one unit more.  A share smaller than
+// kFRMinUnits costs more in joining than it saves.
+// (Units are 16 KB of weight each, so their number is far below 2^31.)
+struct FrShares {
+    int kbt, count, cut, per, more;
+    FrShares() = default;
+    __host__ __device__ __forceinline__ FrShares(int tiles, int kbt_, int ctas, int cut_ = 0) : kbt(kbt_), cut(cut_) {
+        const int units = tiles * kbt;
+        if (cut) {
+            count = cut * tiles;
+            per = more = 0;
+            return;
+        }
+        int most = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
+        if (most > ctas) most = ctas;
+        const int c = tiles <= most ? most / tiles : 0;
+        if (c > 0 && 5 * c * tiles >= 4 * most) cut = c;
+        count = cut ? cut * tiles : most;
+        per = units / count;
+        more = units % count;
+    }
+    // Where share c begins, and its number of units (none for c >= count).  Divisions are few here:
+    // the stream waits for them, and each is 50 ns.
+    __device__ __forceinline__ void locate(int c, int& tile, int& kb, int& n) const {
+        if (c >= count) {
+            tile = kb = n = 0;
+        } else if (cut == 1) {
+            tile = c;
+            kb = 0;
+            n = kbt;
+        } else if (cut) {
+            tile = c / cut;
+            const int piece = c - tile * cut;
+            kb = piece * kbt / cut;
+            n = (piece + 1) * kbt / cut - kb;
+        } else {
+            const int u = start(c);
+            tile = u / kbt;
+            kb = u - tile * kbt;
+            n = per + (c < more ? 1 : 0);
+        }
+    }
+    __device__ __forceinline__ int start(int share) const {
+        if (cut) {
+            const int t = share / cut;
+            return t * kbt + (share - t * cut) * kbt / cut;
+        }
+        return share * per + min(share, more);
+    }
+    __device__ __forceinline__ int owner(int unit) const {
+        if (cut) {
+            const int t = unit / kbt;
+            return t * cut + ((unit - t * kbt + 1) * cut - 1) / kbt;
+        }
+        const int big = more * (per + 1);
+        return unit < big ? unit / (per + 1) : more + (unit - big) / per;
+    }
+};
 
 struct Fp8RowsParams {
     int M;                 // rows of X (tokens)
@@ -98,6 +170,7 @@ struct Fp8RowsParams {
     void* Y;               // kRows, kDown: M x N, 16 bits
     uint8_t* hq;           // kGateUp: codes [a][M][N], scales times routing weights [(a * NB + nb) * M + m]
     float* hs;
+    FrShares shares;       // kRows
     int cut;               // blocks of a cluster that share each tile (1: a tile per block); 0: FrShares' own choice
     int next_grid, next_cut;  // kGateUp: grid and cut of the down product
     float* parts;          // per CTA two slots (kGateUp: four) of part_rows x kA x 128 floats
@@ -107,13 +180,6 @@ struct Fp8RowsParams {
     uint64_t wait_limit_ns;
     uint32_t test_flags;   // bit 0: block 0 never signals its first unit (timeout test)
 };
-
-constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
-constexpr int kFRPrefetch = 10;  // boxes of the next product fetched into L2 per block (24 MB in all)
-// in place of the scale of a row that did not choose the expert (-FLT_MAX: no
-// product of scales is that, whatever a caller's weight scales are)
-constexpr float kFRNotChosen = -3.40282347e38f;
-constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
 
 // 12 warps where the epilogue is 4 (168 registers a thread), 16 where it is 8
 // (128), 20 where it is 16 (96)
@@ -147,48 +213,6 @@ __host__ __device__ constexpr int fr_stages() {
 }
 template <int kMode, int kNT>
 __host__ __device__ constexpr int fr_smem_bytes() { return fr_bytes<kMode, kNT>(fr_stages<kMode, kNT>()); }
-
-// How `tiles` tiles of kbt units are shared out on at most `ctas` CTAs.  Where
-// cutting every tile in the same number of pieces keeps at least 4 of 5 CTAs
-// busy, that is done (`cut` pieces a tile): a CTA then has a part of one tile
-// only, and one SM's stream (56 GB/s of a matrix that is not in L2, whatever
-// the other SMs do) times 118 is still all that HBM gives.  Otherwise equal
-// runs of units, of `per` units each, the first `more` of them one unit more.
-// A share smaller than kFRMinUnits costs more in joining than it saves.
-// (Units are 16 KB of weight each, so their number is far below 2^31.)
-struct FrShares {
-    int kbt, count, cut, per, more;
-    __host__ __device__ __forceinline__ FrShares(int tiles, int kbt_, int ctas, int cut_ = 0) : kbt(kbt_), cut(cut_) {
-        const int units = tiles * kbt;
-        if (cut) {
-            count = cut * tiles;
-            per = more = 0;
-            return;
-        }
-        int most = units / kFRMinUnits > tiles ? units / kFRMinUnits : tiles;
-        if (most > ctas) most = ctas;
-        const int c = tiles < most ? most / tiles : 0;
-        if (c > 0 && 5 * c * tiles >= 4 * most) cut = c;
-        count = cut ? cut * tiles : most;
-        per = units / count;
-        more = units % count;
-    }
-    __device__ __forceinline__ int start(int share) const {
-        if (cut) {
-            const int t = share / cut;
-            return t * kbt + (share - t * cut) * kbt / cut;
-        }
-        return share * per + min(share, more);
-    }
-    __device__ __forceinline__ int owner(int unit) const {
-        if (cut) {
-            const int t = unit / kbt;
-            return t * cut + ((unit - t * kbt + 1) * cut - 1) / kbt;
-        }
-        const int big = more * (per + 1);
-        return unit < big ? unit / (per + 1) : more + (unit - big) / per;
-    }
-};
 
 // silu(g) * u
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -290,7 +314,7 @@ template <int kMode, int kNT, bool kFuse, typename T>
 __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     k_fp8_rows(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_w2,
                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_next,
-               const Fp8RowsParams p) {
+               const __grid_constant__ Fp8RowsParams p) {
     constexpr int kA = fr_a<kMode>();
     constexpr int kStageBytes = fr_stage_bytes<kMode, kNT>();
     constexpr int kStages = fr_stages<kMode, kNT>();
@@ -381,11 +405,13 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     const int kbt = kMode == kDown ? p.KB * n_active : p.KB;  // units per tile
     const int tiles = kMode == kRows ? p.NB * p.MB : kMode == kGateUp ? p.NB * n_active : p.NB;
     const int c = (int)blockIdx.x;
-    const FrShares sh(tiles, kbt, (int)gridDim.x, p.cut);
+    const FrShares own = kMode == kRows ? FrShares() : FrShares(tiles, kbt, (int)gridDim.x, p.cut);
+    const FrShares& sh = kMode == kRows ? p.shares : own;
     const bool clustered = kMode != kGateUp && p.cut > 1;
-    const int C = sh.count;
-    const int nu = c < C ? sh.start(c + 1) - sh.start(c) : 0;  // this CTA's units
-    const int first_tile = sh.start(c) / kbt, first_kb = sh.start(c) - first_tile * kbt;
+    int first_tile, first_kb, nu;  // where this CTA's share begins, and its units
+    sh.locate(c, first_tile, first_kb, nu);
+    const auto by_rows = [&](int tile) { return p.MB == 1 ? tile : tile / p.MB; };  // kRows: a tile's block of channels
+    const auto row0_of = [&](int tile) { return kMode == kRows && p.MB > 1 ? tile % p.MB * kNT : 0; };
     const size_t slot_floats = (size_t)p.part_rows * kA * 128;
 
     // the a-th chosen expert (by a whole warp)
@@ -399,8 +425,8 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     // 4 channels per lane.
     const auto finish_rows = [&](int t, int row0, int step, int cf, int cl, const auto& part_of) {
         constexpr int kR = 4, kO = kA == 2 ? 1 : 4;  // kR rows' loads of kO owners in flight together
-        const int m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
-        const int nb = kMode == kRows ? t / p.MB : kMode == kGateUp ? t % p.NB : t;
+        const int m0 = row0_of(t), rows = min(kNT, p.M - m0);
+        const int nb = kMode == kRows ? by_rows(t) : kMode == kGateUp ? t % p.NB : t;
         const int n = nb * 128 + 4 * lane;
         // kGateUp: rows that did not choose the expert have no sums; their codes are zero
         const unsigned long long mask = kMode == kGateUp ? __ldcg(p.masks + t / p.NB) : ~0ull;
@@ -488,7 +514,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             // where the boxes are: k, channel, and expert or row of X; kept up to date with
             // additions (a division per unit would set the pace of the stream)
             int kb = first_kb;
-            int nb = kMode == kRows ? first_tile / p.MB : kMode == kGateUp ? first_tile - first_a * p.NB : first_tile;
+            int nb = kMode == kRows ? by_rows(first_tile) : kMode == kGateUp ? first_tile - first_a * p.NB : first_tile;
             const int mb0 = kMode == kRows ? first_tile - nb * p.MB : 0;
             int mb = mb0;
             int a = first_a, ib = kMode == kDown ? first_kb - first_a * p.KB : 0, e = first_a < 31 ? first_e : __ldcg(p.active + 1 + first_a);
@@ -669,7 +695,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             }
             left -= seg;
 
-            const int m0 = kMode == kRows ? (tile % p.MB) * kNT : 0;
+            const int m0 = row0_of(tile);
             if (!whole || kMode == kGateUp || clustered) {
                 // this CTA's sums of the tile, [rows][kA][128 channels]; slot 0 for a tile that
                 // began in an earlier share, slot 1 for one that begins here and goes on,
@@ -728,7 +754,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                 }
                 continue;
             }
-            const int n = (kMode == kRows ? tile / p.MB : tile) * 128 + (kBoxA ? ch : c0);
+            const int n = (kMode == kRows ? by_rows(tile) : tile) * 128 + (kBoxA ? ch : c0);
             if constexpr (kBoxA) {
                 if (n < p.N) {
                     uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + n;  // (kNT rows hold all: m0 is 0)
@@ -770,7 +796,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         // ------------------------------------------------ scales, and codes with kFuse
         const int sidx = role - 2;
         int kb = first_kb + sidx;
-        int nb = kMode == kRows ? first_tile / p.MB : kMode == kGateUp ? first_tile % p.NB : first_tile;
+        int nb = kMode == kRows ? by_rows(first_tile) : kMode == kGateUp ? first_tile % p.NB : first_tile;
         int mb = kMode == kRows ? first_tile - nb * p.MB : 0, a = kMode == kGateUp ? first_tile / p.NB : 0;
         const auto settle = [&]() {  // kb counts on from a tile's start: to the tile that it is in
             while (kb >= kbt) {
@@ -849,7 +875,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
             const uint32_t phase = (uint32_t)(i / kStages) & 1u;
             float* s = slots + slot * (kA * kNT);
             if constexpr (kFuse) {
-                static_assert(kMode == kRows && kBoxA, "fused codes: the plain product of at most 32 rows");
+                static_assert(kMode == kRows && kBoxA, "fused codes: the plain product of at most 16 rows");
                 // 8 lanes per row, 16 values each; 4 rows per step
                 const int chunk = lane & 7, rsub = lane >> 3;
                 const int k = kb * 128 + chunk * 16;
@@ -898,8 +924,8 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
     if (clustered) {
         __syncwarp();
         cluster_sync_all();  // everyone's sums are in shared memory
-        const int t = c / p.cut, m0 = kMode == kRows ? (t % p.MB) * kNT : 0, rows = min(kNT, p.M - m0);
-        const int n = (kMode == kRows ? t / p.MB : t) * 128 + 4 * lane;
+        const int t = first_tile, m0 = row0_of(t), rows = min(kNT, p.M - m0);
+        const int n = (kMode == kRows ? by_rows(t) : t) * 128 + 4 * lane;
         constexpr int kWarps = fr_threads<kNT>() / 32;
         const uint32_t at = smem_u32(smem) + (uint32_t)lane * 16;
 #pragma unroll 1
@@ -919,10 +945,12 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
         }
         cluster_sync_all();  // nobody leaves while its sums are read
     }
-    const int end_kb = first_kb + nu;  // the share's end, in units from its first tile's start
-    const int head_tile = nu > 0 && first_kb > 0 ? first_tile : -1;
-    const int tail_tile =
-        nu > 0 && end_kb % kbt != 0 && (first_kb == 0 || end_kb > kbt) ? first_tile + end_kb / kbt : -1;
+    int head_tile = -1, tail_tile = -1;
+    if (nu > 0 && sh.cut != 1) {
+        const int end_kb = first_kb + nu;  // the share's end, in units from its first tile's start
+        if (first_kb > 0) head_tile = first_tile;
+        if (end_kb % kbt != 0 && (first_kb == 0 || end_kb > kbt)) tail_tile = first_tile + end_kb / kbt;
+    }
     if (!clustered && role != 0 && role != 1 && (head_tile >= 0 || tail_tile >= 0)) {
         named_bar_sync(1, 32 * kJoinWarps);
         if (warp == 0) {  // lane 0: the head's ticket, lane 1: the tail's

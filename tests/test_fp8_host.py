@@ -67,7 +67,7 @@ def test_forward_refusals(lib):
 
 
 def test_overlapping_buffers_are_refused(lib):
-    """Up to 32 rows are quantised while other blocks store results, so Y may not
+    """A few rows are quantised while other blocks store results, so Y may not
     lie on X; nor may codes or scales lie on X or on one another."""
     assert _quant(lib, codes=FAKE) == 1 and _quant(lib, codes=FAKE + 2032) == 1  # X: 4 x 256 values, 2048 bytes
     assert _quant(lib, codes=FAKE + 4096, scales=FAKE + 2044) == 1

@@ -160,6 +160,42 @@ def test_product_forced_paths(cuda_ok, M, K, N, path):
     _check(Y, X, w)
 
 
+@pytest.mark.parametrize("M,K,N", [
+    (8, 8192, 1024),      # few tiles: a cluster's blocks take pieces of one
+    (16, 1040, 144),
+    (3, 16384, 272),
+    (24, 4112, 528),
+    (31, 528, 4112),      # a tile per block
+    (40, 2064, 400),
+    (100, 528, 1040),
+    (128, 8208, 272),
+    (8, 2064, 20496),     # more tiles than SMs: runs that begin and end inside tiles
+    (30, 784, 20496),
+    (50, 400, 19216),
+    (120, 272, 19216),
+])
+def test_product_however_tiles_are_shared_out(cuda_ok, M, K, N):
+    X, w = _case(M, K, N, torch.bfloat16, K + N + M)
+    ws = i8.Fp8Workspace(M, K, N)
+    Y = i8.forward_fp8(X.cuda(), w, workspace=ws)
+    assert i8.device_status(ws)[0] == 0
+    _check(Y, X, w)
+    assert torch.equal(i8.forward_fp8(X.cuda(), w, workspace=ws), Y)
+
+
+@pytest.mark.parametrize("M", [8, 24, 60])
+def test_wait_limit_in_a_cluster_reports_timeout_and_recovers(cuda_ok, M):
+    K, N = 8192, 256
+    X, w = _case(M, K, N, torch.float16, 31)
+    Xd, ws = X.cuda(), i8.Fp8Workspace(M, K, N)
+    want = i8.forward_fp8(Xd, w, workspace=ws)
+    i8.forward_fp8(Xd, w, workspace=ws, wait_limit_ns=50_000_000, test_flags=1)
+    assert i8.device_status(ws)[0] == 6
+    ws.reset()
+    assert torch.equal(i8.forward_fp8(Xd, w, workspace=ws), want)
+    assert i8.device_status(ws)[0] == 0
+
+
 @pytest.mark.parametrize("path,M", [("decode", 5), ("decode", 20), ("decode", 40), ("decode", 150), ("gemm", 300)])
 def test_rows_that_are_not_finite_stay_alone(cuda_ok, path, M):
     K, N = 656, 272
