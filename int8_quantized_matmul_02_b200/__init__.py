@@ -536,8 +536,8 @@ def forward_fp8(X: torch.Tensor, w: Fp8Weight, *, out: torch.Tensor | None = Non
                 stream=None) -> torch.Tensor:
     """Y = X W with X (M x K float16 or bfloat16, on the weight's device)
     quantised to e4m3 per row and block of 128 by the call, and the
-    block-scaled weight; fp32 sums, Y in X's type.  path: "auto", "gemm"
-    (tiled) or "decode" (weight-streaming, M <= 1024)."""
+    block-scaled weight; fp32 sums, Y in X's type.  out must not overlap X.
+    path: "auto", "gemm" (tiled) or "decode" (weight-streaming, M <= 1024)."""
     dev = w.device
     if X.dtype not in _DTYPES or X.dim() != 2 or X.shape[1] != w.K or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous float16 or bfloat16 tensor of shape (M, {w.K}) on {dev}")
@@ -633,9 +633,9 @@ def forward_moe_fp8(X: torch.Tensor, w: MoeFp8Weight, top_k: int, *, renormalize
     """The mixture-of-experts layer on a few tokens: X is T x H (T <= 64) in the
     router's type and on its device.  Each token takes the top_k experts of
     softmax(X router^T), ties to the lower index, with those probabilities as
-    weights (renormalize: divided by their sum).  Returns Y, T x H in X's type,
-    and with return_routing also the experts (int32 T x top_k, best first) and
-    their weights (float32 T x top_k)."""
+    weights (renormalize: divided by their sum); out may be X.  Returns Y, T x H
+    in X's type, and with return_routing also the experts (int32 T x top_k, best
+    first) and their weights (float32 T x top_k)."""
     dev = w.device
     if X.dtype != w.router.dtype or X.dim() != 2 or X.shape[1] != w.H or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous {w.router.dtype} tensor of shape (T, {w.H}) on {dev}")

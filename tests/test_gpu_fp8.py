@@ -3,6 +3,10 @@ reference (tests/fp8_reference.py, where the tolerances are derived): codes and
 scales bit for bit, Y within its bound."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -248,6 +252,50 @@ def test_new_weights_in_place_are_seen_by_the_next_call(cuda_ok):
         w.codes.view(torch.uint8).copy_(saved.view(torch.uint8))
         a = i8.forward_fp8(Xd, w, workspace=ws)
         assert torch.equal(b, -first) and torch.equal(a, first)
+
+
+@pytest.mark.parametrize("M", [3, 24, 100, 400, 1100])
+def test_weights_and_rows_written_just_before_the_call(cuda_ok, M):
+    """The kernels start while earlier ones end; what those wrote is read all the same."""
+    K, N = 1040, 2064
+    X, w = _case(M, K, N, torch.float16, 41)
+    Xd, ws = X.cuda(), i8.Fp8Workspace(M, K, N)
+    filler = torch.zeros(1 << 24, device="cuda")
+    codes = [w.codes.view(torch.uint8).roll(k, 1).contiguous() for k in range(4)]
+    rows = [Xd.roll(k, 0).contiguous() for k in range(4)]
+    want = []
+    for k in range(4):
+        want.append(i8.forward_fp8(rows[k], i8.weight_fp8(codes[k].view(torch.float8_e4m3fn), w.scales)))
+        torch.cuda.synchronize()
+    got, x = [], torch.empty_like(Xd)
+    for k in range(4):
+        filler.add_(1)
+        x.copy_(rows[k])
+        w.codes.view(torch.uint8).copy_(codes[k])
+        got.append(i8.forward_fp8(x, w, workspace=ws))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_the_first_call_of_a_process_may_be_captured(cuda_ok):
+    """Nothing that a first call sets up (kernel attributes, occupancy) is barred while a graph is captured."""
+    code = """
+import torch, int8_quantized_matmul_02_b200 as i8
+g = torch.Generator(device="cuda").manual_seed(1)
+codes = torch.randint(0, 120, (1024, 8192), dtype=torch.uint8, device="cuda", generator=g).view(torch.float8_e4m3fn)
+w = i8.weight_fp8(codes, torch.rand(8, 64, device="cuda", generator=g))
+xs = [torch.randn(M, 8192, device="cuda", generator=g).half() for M in (8, 24, 50, 100, 1030)]
+wss = [i8.Fp8Workspace(x.shape[0], 8192, 1024) for x in xs]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    ys = [i8.forward_fp8(x, w, workspace=s) for x, s in zip(xs, wss)]
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(y, i8.forward_fp8(x, w)) for x, y in zip(xs, ys))
+print("same")
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
 
 
 @pytest.mark.parametrize("M", [8, 40, 300])

@@ -154,6 +154,32 @@ def test_another_stream_and_a_captured_call(cuda_ok):
         assert torch.equal(Ys, eager)
 
 
+@pytest.mark.parametrize("T", [2, 20, 60])
+def test_weights_and_tokens_written_just_before_the_call(cuda_ok, T):
+    """The kernels start while earlier ones end; what those wrote is read all the same."""
+    X, w = _case(T, 8, 528, 272, torch.float16, 12)
+    Xd, ws = X.cuda(), i8.MoeWorkspace(T, w, 3)
+    filler = torch.zeros(1 << 24, device="cuda")
+    parts = [w.router, *(p.view(torch.uint8) for p, _ in (w.gate, w.up, w.down)), Xd]
+    kept = [[p.roll(k, 0).contiguous() for p in parts] for k in range(4)]
+
+    def write(k):
+        for p, v in zip(parts, kept[k]):
+            p.copy_(v)
+
+    want, got = [], []
+    for k in range(4):
+        write(k)
+        torch.cuda.synchronize()
+        want.append(i8.forward_moe_fp8(Xd, w, 3))
+        torch.cuda.synchronize()
+    for k in range(4):
+        filler.add_(1)
+        write(k)
+        got.append(i8.forward_moe_fp8(Xd, w, 3, workspace=ws))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_two_calls_at_once(cuda_ok):
     X, w = _case(16, 16, 512, 512, torch.bfloat16, 6)
     Xd = X.cuda()
