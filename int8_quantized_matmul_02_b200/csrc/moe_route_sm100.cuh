@@ -98,15 +98,26 @@ __global__ void __launch_bounds__(kRouteThreads)
             }
         }
     }
+    // Sums over the warp: at each step a lane gives half of its values to its
+    // partner and keeps the other half (16 exchanges for 16 values, not 80).
+    constexpr int kV = kRouteExperts * kTT;
+    double v[kV];
 #pragma unroll
-    for (int i = 0; i < kRouteExperts; ++i)
+    for (int i = 0; i < kV; ++i) v[i] = acc[i / kTT][i % kTT];
+    int which = 0, d = 16;  // this lane's value in the end
 #pragma unroll
-        for (int j = 0; j < kTT; ++j) {
-            double a = acc[i][j];
+    for (int n = kV / 2; n >= 1; n >>= 1, d >>= 1) {
+        const bool up = lane & d;
+        which += up ? n : 0;
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-            if (lane == 0) red[warp][i * kTT + j] = a;
+        for (int i = 0; i < n; ++i) {
+            const double give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
         }
+    }
+#pragma unroll
+    for (; d >= 1; d >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+    if ((lane & (32 / kV - 1)) == 0) red[warp][which] = v[0];
     __syncthreads();
     if (tid < kRouteExperts * kTT) {
         const int e = e0 + tid / kTT, t = t0 + tid % kTT;
