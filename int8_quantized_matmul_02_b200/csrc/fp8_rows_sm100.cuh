@@ -25,11 +25,11 @@
 // blocks take equal pieces of one; the caller decides (`cut`).  Otherwise the
 // units, ordered by output tile and then k, are cut into equal consecutive
 // shares, one per CTA (one CTA per SM): a CTA's share may start and end inside
-// a tile.  Of a tile that several CTAs share every one
-// stores its fp32 sums; at the end of its share, so that the stream is never
-// held up, each takes a ticket for its first and last tile, and the last one
-// to come adds the stored sums in the order of k: the result does not depend
-// on who that is, and no CTA waits for another.
+// a tile.  Of a tile that several CTAs share every one stores its fp32 sums; at
+// the end of its share, so that the stream is never held up, each takes a
+// ticket for its first and last tile, and the last one to come adds the stored
+// sums in the order of k: the result does not depend on who that is, and no
+// CTA waits for another.
 //
 // That join takes 2 us for 8 rows and 9 for 128 (one block reads all the
 // others' sums).  The blocks of a cluster leave their sums in shared memory and
@@ -46,8 +46,8 @@
 //            a token's experts happens in the same running sums.
 // In the gated layer every token is a row for every expert.  Of tokens that did
 // not choose an expert kGateUp stores zero codes, and kDown leaves out what the
-// accumulators hold for them there (kFRNotChosen): an infinity or a NaN
-// in an expert's weights reaches the tokens that chose it and no other.
+// accumulators hold for them there (kFRNotChosen): an infinity or a NaN in an
+// expert's weights reaches the tokens that chose it and no other.
 //
 // Warps: the epilogue is warps 0-3 (a TMEM lane quadrant of channels each) for
 // kNT <= 32; above, with rows in kQ quadrants, the warps w with w % 4 < kQ
@@ -66,10 +66,10 @@
 // Measured (calls back to back, weights from HBM): 1 x 12288 x 49152 95 us, 6.36
 // TB/s, which is what HBM gives; 8 x 4096 x 11008 12.0 us, of which 9 are the
 // stream of 86 blocks (56 to 60 GB/s each) and the rest the start and the first
-// boxes' latency; 16 x 256 x 384 3.8 us, all start;
-// 100 x 11008 x 4096 18.5 us and 333 x 4112 x 5136 20.6 us, bound by shared memory
-// (a unit of 128 rows writes and reads 32 KB each way, 512 cycles at 128 bytes
-// a cycle, and takes ~670).  The gate/up kernel streams at 6.2 to 7 TB/s.
+// boxes' latency; 16 x 256 x 384 3.8 us, all start; 100 x 11008 x 4096 18.5 us
+// and 333 x 4112 x 5136 20.6 us with the quantiser before, bound by shared
+// memory (a unit of 128 rows writes and reads 32 KB each, 512 cycles at 128
+// bytes a cycle, and takes ~670).  The gate/up kernel streams at 6.2 to 7 TB/s.
 #pragma once
 
 #include "fp8_common.cuh"
