@@ -81,9 +81,12 @@ enum { kRows = 0, kGateUp = 1, kDown = 2 };
 
 constexpr int kFRMinUnits = 4;   // a share smaller than this costs more in joining than it saves
 constexpr int kFRPrefetch = 10;  // boxes of the next product fetched into L2 per block (24 MB in all)
-// in place of the scale of a row that did not choose the expert (-FLT_MAX: no
-// product of scales is that, whatever a caller's weight scales are)
-constexpr float kFRNotChosen = -3.40282347e38f;
+// In place of the scale of a row that did not choose the expert: the bits of -0.
+// No scale of h is that (it is 2^-126 at least, times a weight that is not
+// negative), and kDown adds +0 to its scale products, which turns a -0 into +0
+// and leaves every other number as it is, whatever a caller's weight scales are.
+constexpr uint32_t kFRNotChosen = 0x80000000u;
+__device__ __forceinline__ bool fr_not_chosen(float s) { return __float_as_uint(s) == kFRNotChosen; }
 constexpr int kFRMaxCtas = 160;  // shares (a fixed bound, so that the workspace depends on the shape only)
 
 // How `tiles` tiles of kbt units are shared out on at most `ctas` CTAs: `cut`
@@ -258,10 +261,10 @@ __device__ __forceinline__ void fma_scaled(uint64_t* v, const uint32_t* r, const
         for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(r[4 * i + j]);
         if constexpr (kSkip) {
             const float2 lo = f32x2_parts(f.x), hi = f32x2_parts(f.y);
-            x[0] = lo.x == kFRNotChosen ? 0.0f : x[0];
-            x[1] = lo.y == kFRNotChosen ? 0.0f : x[1];
-            x[2] = hi.x == kFRNotChosen ? 0.0f : x[2];
-            x[3] = hi.y == kFRNotChosen ? 0.0f : x[3];
+            x[0] = fr_not_chosen(lo.x) ? 0.0f : x[0];
+            x[1] = fr_not_chosen(lo.y) ? 0.0f : x[1];
+            x[2] = fr_not_chosen(hi.x) ? 0.0f : x[2];
+            x[3] = fr_not_chosen(hi.y) ? 0.0f : x[3];
         }
         fma_f32x2(v[2 * i], f32x2(x[0], x[1]), f.x);
         fma_f32x2(v[2 * i + 1], f32x2(x[2], x[3]), f.y);
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                     // the scale that the down product adds the row with: the routing weight in it
                     const unsigned by = __ballot_sync(0xffffffffu, !(wt[r] < 0.0f));
                     const float w = __shfl_sync(0xffffffffu, wt[r], by ? __ffs(by) - 1 : 0);
-                    if (lane == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? __fmul_rn(s, w) : kFRNotChosen;
+                    if (lane == 0) p.hs[((size_t)a * p.NB + nb) * p.M + row] = chosen ? __fmul_rn(s, w) : __uint_as_float(kFRNotChosen);
                 } else if (n < p.N) {  // N % 16 == 0
                     const float4 x = sum[r][0];
                     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.Y) + (size_t)(m0 + row) * p.N + n) =
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
                         uint32_t r[32];
                         tmem_ld32(t + (uint32_t)(a * kCols), r);
                         seen = tmem_wait_ld_look(r, &done[next], next_phase);
-                        if (kMode != kDown || s1 != kFRNotChosen) fma32(v[a], r, f32x2(s1, s1));
+                        if (kMode != kDown || !fr_not_chosen(s1)) fma32(v[a], r, f32x2(s1, s1));
                         if (kA == 2) pin16(v[a]);  // these FMAs first: the next load's registers are these
                     } else {
                         const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(slots + (slot * kA + a) * kNT);
@@ -854,9 +857,11 @@ __global__ void __launch_bounds__(fr_threads<kNT>(), 1)
 #pragma unroll
                     for (int b = 0; b < kA; ++b)
 #pragma unroll
-                        for (int j = 0; j < kPer; ++j)
-                            f[b][j] = kMode == kDown && ax[d][j] == kFRNotChosen ? kFRNotChosen
-                                                                                 : __fmul_rn(ax[d][j], aw[d][b]);
+                        for (int j = 0; j < kPer; ++j) {
+                            f[b][j] = __fmul_rn(ax[d][j], aw[d][b]);
+                            if (kMode == kDown)  // the mark stays, and no product is the mark
+                                f[b][j] = fr_not_chosen(ax[d][j]) ? ax[d][j] : __fadd_rn(f[b][j], 0.0f);
+                        }
                     if (i + kDeep * kSide < end) load(d);
                     ok = __all_sync(0xffffffffu, wait_fast(&done[stage], ((uint32_t)(i / kStages) & 1u) ^ 1u, wctx));
                     if (!ok) continue;

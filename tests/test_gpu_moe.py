@@ -125,6 +125,32 @@ def test_weights_that_are_not_finite_reach_their_own_tokens_only(cuda_ok, T, whi
     assert not torch.isfinite(Y[chose]).all(1).any()
 
 
+@pytest.mark.parametrize("T", [3, 20, 50])
+def test_a_down_scale_of_any_value_counts(cuda_ok, T):
+    """The lowest fp32 number as an expert's down scale, next to a scale of h of
+    exactly one: its tokens get that multiple of their sums, the other expert's
+    tokens theirs.  Every step is exact: g = 64 (silu(64) = 64 in fp32), u = 7,
+    h = 448 with scale 1, the sum 448 * 2^-9 = 0.875, and bf16 holds 0.875 and
+    0.875 * 2^128; -0.875 * FLT_MAX rounds to the latter's negative."""
+    H = I = 128
+    one = {v: int(torch.tensor(float(v)).to(torch.float8_e4m3fn).view(torch.uint8)) for v in (64, 7, 2.0 ** -9)}
+    gate, up, down = (torch.zeros(2, 128, 128, dtype=torch.uint8, device="cuda") for _ in range(3))
+    gate[:, 0, 1], up[:, 0, 1], down[:, :, 0] = one[64], one[7], one[2.0 ** -9]
+    scales = [torch.ones(2, 1, 1, device="cuda") for _ in range(3)]
+    scales[2][0] = torch.finfo(torch.float32).min
+    router = torch.zeros(2, H, dtype=torch.bfloat16, device="cuda")
+    router[0, 2], router[1, 2] = 8, -8
+    w = i8.moe_weight_fp8(router, *((c.view(torch.float8_e4m3fn), s) for c, s in zip((gate, up, down), scales)))
+    X = torch.zeros(T, H, dtype=torch.bfloat16)
+    X[:, 0], X[:, 1] = 448, 1                 # the block's scale is 1; the gate and up weights read column 1
+    X[:, 2] = 1
+    X[1::2, 2] = -1                           # every other token chooses expert 1
+    Y, ids, wts = i8.forward_moe_fp8(X.cuda(), w, 1, return_routing=True)
+    assert ids.flatten().tolist() == [t % 2 for t in range(T)] and (wts == 1).all()
+    assert (Y[1::2].double() == 0.875).all()
+    assert (Y[::2].double() == -0.875 * 2.0 ** 128).all()
+
+
 def test_output_in_place_of_the_tokens(cuda_ok):
     X, w = _case(7, 8, 272, 256, torch.float16, 11)
     Xd = X.cuda()
