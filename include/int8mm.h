@@ -452,8 +452,9 @@ size_t int8mm_moe_workspace_bytes(int T, int H, int I, int E, int top_k);
  * topk_ids (device, T x top_k int32, best first) and topk_weights (device,
  * T x top_k fp32) receive the routing; each may be NULL.  Only the weights of
  * chosen experts are read, and an infinity or a NaN in an expert's weights
- * reaches the tokens that chose it and no other.  Y may be X.  opts may be
- * NULL; path and events must be unset. */
+ * reaches the tokens that chose it and no other.  Y may be X or overlap it;
+ * otherwise Y, topk_ids, topk_weights and ws overlap neither one another nor X
+ * or the weights.  opts may be NULL; path and events must be unset. */
 int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const int8mm_moe_weight* w, int top_k,
                                      int renormalize, uint16_t* Y, int32_t* topk_ids, float* topk_weights, void* ws,
                                      size_t ws_bytes, const int8mm_forward_opts* opts, void* stream);

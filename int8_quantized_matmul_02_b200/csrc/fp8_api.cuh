@@ -413,6 +413,23 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
         return INT8MM_ERR_MISALIGNED;
     const MoeWsLayout L = moe_ws_layout(T, H, I, E, top_k);
     if (ws_bytes < L.total) return INT8MM_ERR_WORKSPACE_TOO_SMALL;
+    // What the kernels write lies on nothing else (the lists in the workspace and topk_ids are
+    // indexes that later blocks use, and routing is stored while other blocks still read X); only
+    // Y, which is written last, may lie on X.
+    const size_t values = (size_t)E * H * I, block_scales = (size_t)E * cdiv(H, 128) * cdiv(I, 128) * 4;
+    const size_t routed = (size_t)T * top_k * 4, tokens = (size_t)T * H * 2;
+    const struct {
+        const void* at;
+        size_t bytes;
+    } parts[] = {{ws, L.total}, {topk_ids, topk_ids ? routed : 0}, {topk_weights, topk_weights ? routed : 0}, {Y, tokens},
+                 {X, tokens}, {w->router, (size_t)E * H * 2}, {w->gate_codes, values}, {w->up_codes, values},
+                 {w->down_codes, values}, {w->gate_scales, block_scales}, {w->up_scales, block_scales},
+                 {w->down_scales, block_scales}};
+    constexpr int kWritten = 4, kY = 3, kX = 4;
+    for (int i = 0; i < kWritten; ++i)
+        for (int j = i + 1; parts[i].bytes && j < (int)(sizeof(parts) / sizeof(parts[0])); ++j)
+            if (!(i == kY && j == kX) && parts[j].bytes && overlap(parts[i].at, parts[i].bytes, parts[j].at, parts[j].bytes))
+                return INT8MM_ERR_INVALID_ARGUMENT;
     int dev;
     DeviceInfo* info;
     int8mm_status st = current_device(&dev, &info);

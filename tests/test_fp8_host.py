@@ -122,6 +122,41 @@ def test_moe_refusals(lib):
     assert lib.int8mm_moe_workspace_bytes(4, 256, 384, 8, 9) == 0
 
 
+def test_overlapping_buffers_of_the_layer_are_refused(lib):
+    """Routing is stored while X is read, and what lies in topk_ids and in the
+    workspace is used as an index: nothing that is written lies on anything
+    else, but for Y on X.  Calls that pass get as far as the device, which is
+    not there (the pointers are not memory, so where there is one this test
+    makes no such call)."""
+    T, E, H, I, k = 4, 8, 256, 384, 2
+    MB = 1 << 20
+    names = ("router", "gate_codes", "gate_scales", "up_codes", "up_scales", "down_codes", "down_scales")
+    size = {"router": E * H * 2, "gate_codes": E * H * I, "up_codes": E * H * I, "down_codes": E * H * I,
+            "gate_scales": E * 6 * 4, "up_scales": E * 6 * 4, "down_scales": E * 6 * 4, "X": T * H * 2, "Y": T * H * 2,
+            "ids": T * k * 4, "wts": T * k * 4, "ws": lib.int8mm_moe_workspace_bytes(T, H, I, E, k)}
+    apart = {n: FAKE + 64 * MB * i for i, n in enumerate(size)}
+    assert max(size.values()) < 64 * MB
+
+    def call(**moved):
+        at = {**apart, **moved}
+        return _moe(lib, X=at["X"], T=T, w=_moe_weight(E, H, I, **{n: at[n] for n in names}), top_k=k, Y=at["Y"],
+                    ids=at["ids"], wts=at["wts"], ws=at["ws"], nbytes=size["ws"])
+
+    for a in ("ids", "wts", "Y", "ws"):
+        for b in size:
+            if a == b or {a, b} == {"X", "Y"}:
+                continue
+            step = 256  # keeps every alignment
+            assert call(**{a: apart[b]}) == 1, (a, b)
+            assert call(**{a: apart[b] + (size[b] - 1) // step * step}) == 1, (a, b)
+            assert call(**{a: apart[b] - (size[a] - 1) // step * step}) == 1, (a, b)
+    if not torch.cuda.is_available():
+        for fine in ({}, {"Y": apart["X"]}, {"Y": apart["X"] + 1024}, {"ids": None}, {"wts": None},
+                     {"ids": None, "wts": None}, {"ids": apart["X"] + size["X"]}, {"wts": apart["ids"] + size["ids"]},
+                     {"wts": apart["ids"] - size["wts"]}):
+            assert call(**fine) in (4, 5), fine
+
+
 def test_python_front_refuses(lib):
     """Tensors on the CPU, wrong types, shapes and strides: an error before any call."""
     with pytest.raises(ValueError):
