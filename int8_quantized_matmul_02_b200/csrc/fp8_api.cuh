@@ -296,8 +296,8 @@ int8mm_status int8mm_forward_fp8(const uint16_t* X, int dtype, int M, const int8
     if (o.path != INT8MM_PATH_AUTO && o.path != INT8MM_PATH_GEMM && o.path != INT8MM_PATH_DECODE)
         return INT8MM_ERR_INVALID_ARGUMENT;
     if (o.path == INT8MM_PATH_DECODE && M > kFp8RowsMaxM) return INT8MM_ERR_INVALID_ARGUMENT;
-    // tiles and 16 KB units are counted in 32 bits (more of them than any GPU's memory holds)
-    if ((long long)cdiv(N, 128) * cdiv(M, 32) * cdiv(K, 128) > (INT32_MAX >> 4) && M <= kFp8RowsMaxM)
+    // tiles and 16 KB units are counted in 32 bits (units of at most 8 row blocks: a weight of 2 TB)
+    if (M <= kFp8RowsMaxM && (long long)cdiv(N, 128) * cdiv(M, fp8_rows_nt(M)) * cdiv(K, 128) > (INT32_MAX >> 1))
         return INT8MM_ERR_INVALID_ARGUMENT;
     if ((long long)cdiv(N, 128) * cdiv(M, kF8BM) > (INT32_MAX >> 1)) return INT8MM_ERR_INVALID_ARGUMENT;
     if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(ws, 256) || !aligned(w->codes, 16) || !aligned(w->scales, 4))

@@ -66,6 +66,16 @@ def test_forward_refusals(lib):
         assert _fwd(lib, M=M, nbytes=need - 1) == 3
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not memory")
+@pytest.mark.parametrize("M", [1, 100, 1000, 1024, 1025])
+def test_a_weight_that_fills_the_memory_is_not_refused(lib, M):
+    """131072 x 1048576, 128 GB of codes: the call gets as far as the device, which is not there."""
+    K, N, GB = 131072, 1 << 20, 1 << 30
+    assert lib.int8mm_fp8_workspace_bytes(M, K, N) > 0
+    w = _weight(K, N, codes=FAKE, scales=FAKE + 130 * GB)
+    assert _fwd(lib, M=M, w=w, X=FAKE + 140 * GB, Y=FAKE + 150 * GB, ws=FAKE + 160 * GB) in (4, 5)
+
+
 def test_overlapping_buffers_are_refused(lib):
     """A few rows are quantised while other blocks store results, so Y may not
     lie on X; nor may codes or scales lie on X or on one another."""
