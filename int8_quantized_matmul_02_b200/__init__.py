@@ -20,6 +20,10 @@ mixture-of-experts layer of them for a few tokens:
     Y  = forward_fp8(X_MxK, w8, workspace=Fp8Workspace(M, K, N))
     m  = prepare_moe_weight_fp8(router, gate, up, down)
     Y  = forward_moe_fp8(X_TxH, m, top_k, workspace=MoeWorkspace(T, m, top_k))
+
+These e4m3 calls take stream=s as a ``with torch.cuda.stream(s)`` around them
+does: s has to wait for whatever wrote the inputs, and what a call allocates
+belongs to s.  The memory of what a call is given is kept until s is done.
 """
 from __future__ import annotations
 
@@ -406,13 +410,18 @@ _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream  # of a device, as the integer that the C interface takes
 
 
-def _on(device: torch.device, stream=None):
+def _on(device: torch.device, stream, *used):
     """A context with `device` current, and `stream` if given, so that what a
-    call allocates belongs to the stream that it launches on."""
+    call allocates belongs to the stream that it launches on.  `used` (tensors,
+    or None) are what the call takes: their memory, which may belong to another
+    stream, is not given out again before `stream` is done with it."""
     if stream is None:
         return torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    for t in used:
+        if t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -437,7 +446,7 @@ def quantize_fp8(X: torch.Tensor, codes: torch.Tensor | None = None, scales: tor
         raise ValueError("X must be a contiguous 2-D float16 or bfloat16 CUDA tensor")
     dev = X.device
     if stream is not None or _current_device() != dev.index:
-        with _on(dev, stream):
+        with _on(dev, stream, X, codes, scales):
             return quantize_fp8(X, codes, scales)
     M, K = X.shape
     kb = (K + 127) // 128
@@ -501,7 +510,7 @@ def prepare_weight_fp8(W: torch.Tensor, stream=None) -> Fp8Weight:
     if nbytes == 0:
         raise Int8mmError(1, f"int8mm_fp8_weight_bytes(K={K}, N={N})")
     st = _abi.Fp8Weight()
-    with _on(W.device, stream):
+    with _on(W.device, stream, W):
         buf = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
         _abi.check(lib.int8mm_prepare_weight_fp8(W.data_ptr(), _DTYPES[W.dtype], K, N, buf.data_ptr(), nbytes,
                                                  ctypes.byref(st), _current_stream(W.device.index)),
@@ -542,7 +551,7 @@ def forward_fp8(X: torch.Tensor, w: Fp8Weight, *, out: torch.Tensor | None = Non
     if X.dtype not in _DTYPES or X.dim() != 2 or X.shape[1] != w.K or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous float16 or bfloat16 tensor of shape (M, {w.K}) on {dev}")
     if stream is not None or _current_device() != dev.index:
-        with _on(dev, stream):
+        with _on(dev, stream, X, w.codes, w.scales, out, workspace and workspace.buf):
             return forward_fp8(X, w, out=out, workspace=workspace, path=path, wait_limit_ns=wait_limit_ns,
                                test_flags=test_flags)
     M = X.shape[0]
@@ -640,7 +649,7 @@ def forward_moe_fp8(X: torch.Tensor, w: MoeFp8Weight, top_k: int, *, renormalize
     if X.dtype != w.router.dtype or X.dim() != 2 or X.shape[1] != w.H or X.device != dev or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous {w.router.dtype} tensor of shape (T, {w.H}) on {dev}")
     if stream is not None or _current_device() != dev.index:
-        with _on(dev, stream):
+        with _on(dev, stream, X, w.router, *w.gate, *w.up, *w.down, out, workspace and workspace.buf):
             return forward_moe_fp8(X, w, top_k, renormalize=renormalize, out=out, workspace=workspace,
                                    return_routing=return_routing, wait_limit_ns=wait_limit_ns, test_flags=test_flags)
     T = X.shape[0]
