@@ -195,8 +195,10 @@ bool fp8_opts(const int8mm_forward_opts* o, Fp8Opts* out) {
 // of units that are joined through memory.  A tile has `units` units, at least
 // `least` of them (they differ where the device decides on the experts).
 // More tiles than SMs: runs.  Else the shortest by an estimate, whose figures
-// are fits to K = 512 .. 16384, N = 1024 .. 18432 with 8, 24, 48 and 100 rows;
-// there its choice was within 4 % of the best one.  Runs against this choice:
+// are fits to the plain product at K = 512 .. 16384, N = 1024 .. 18432 with 8, 24,
+// 48 and 100 rows; there its choice was within 4 % of the best one.  (It takes a
+// stream for faster than one block's from HBM, 280 ns a unit, and runs for as many
+// shares as there are SMs: see the down product's use of it.)  Runs against this choice:
 // 8 rows, 4096 x 11008 13.7 -> 12.6 us (not cut), 8192 x 1024 11.4 -> 7.1 (8
 // pieces), 1024 x 14336 8.4 -> 6.4 (not cut); 100 rows, 4096 x 11008 23.0 ->
 // 18.5 (not cut), 11008 x 4096 24.0 -> 18.9 (4 pieces), but 16384 x 9728 stays
@@ -506,8 +508,12 @@ int8mm_status int8mm_forward_moe_fp8(const uint16_t* X, int dtype, int T, const 
     const int ggrid = std::min(ctas, std::max(A * IB, A * IB * HB / kFRMinUnits));
     // (the chosen experts are at least top_k)
     g.next_cut = fp8_cut(info, HB, A * IB, top_k * IB, nt, ctas);
-    // (few clusters that leave SMs idle lose against runs here: 16 tokens, 8 of 64 experts,
-    // 2048 x 1408, 6 pieces of 16 tiles 95.1 us, runs 90.6)
+    // Clusters that leave SMs idle lose against runs where much weight is read (us a layer, clusters
+    // against runs: 16 tokens, 8 of 64 experts, 2048 x 1408, 104.2 / 99.6; 8 of 128, 2048 x 768,
+    // 88.2 / 84.2; 32 tokens 121.9 / 114.1 and 117.6 / 110.4).  The rule does not look at how much
+    // that is, and smaller layers lose by it (16 tokens, 2 of 8, 256 x 512, 18.3 / 21.0; 512 x 1408,
+    // 20.4 / 27.4; 1024 x 2816, 33.9 / 38.0; 8 of 64, 512 x 256, 26.0 / 32.6; one token, 2 of 8,
+    // 4096 x 272, 20.9 / 23.3).
     if (nt <= 32 && 5 * g.next_cut * HB < 4 * ctas) g.next_cut = 0;
     g.next_grid = g.next_cut ? g.next_cut * HB : std::min(ctas, std::max(HB, A * IB * HB / kFRMinUnits));
     e = nt == 16   ? launch_rows<kGateUp, 16, false, F16>(dev, ggrid, tg, tu, tx, td, g, s, true)

@@ -15,9 +15,10 @@
 // adding (~300), release seen by the issuing thread (~220), issue (~150).
 // With two accumulators a block takes half of that, ~850 cycles, against the
 // MMAs' 565; TMEM (512 columns) holds no third.  4096 x 12288 x 49152 takes
-// 2.26 ms (2.19 PFLOP/s, 0.66 of twice the measured bf16 rate) and 2048 x 8192
-// x 28672 0.457 ms in short runs; in runs of seconds the power cap holds the
-// clock near 1.4 GHz, and they take 2.75 and 0.55 ms.  Measured and not kept,
+// 2.31 ms (2.14 PFLOP/s, 0.65 of twice the measured bf16 rate) and 2048 x 8192
+// x 28672 0.465 ms in runs of 20 ms; in runs of seconds the power cap holds the
+// clock at 1.43 and 1.51 GHz, and they take 2.68 to 2.79 and 0.54 to 0.55 ms.
+// (Other boxes: 2.26 to 2.40 and 0.457 to 0.482 in short runs.)  Measured and not kept,
 // for the first (2.22 ms then and there): the two column halves as separate
 // accumulators of 128 columns (2.48 ms: MMAs of N = 128 run at a lower rate);
 // 16 epilogue warps of 64 columns (2.41 ms: more threads to see the

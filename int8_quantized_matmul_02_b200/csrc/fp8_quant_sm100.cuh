@@ -8,9 +8,10 @@
 // loads of a warp are whole lines); its maximum takes packed 16-bit
 // instructions and three shuffles, its scale no division, and where the next
 // block lies is found by additions.  kQuantBlocks blocks are in flight per
-// group of 8 lanes.  4096 x 12288: 25.8 us, 5.9 TB/s (0.90 of a plain copy);
-// with divisions for a block's scale and position and 16 lanes a block it was
-// 40.7 us, bound by issue.
+// group of 8 lanes.  4096 x 12288: 25.8 us a launch, 5.9 TB/s (0.90 of a plain
+// copy); calls back to back 26.5 us in runs of 20 ms (0.88), 27.6 us in runs of
+// seconds (0.84, at 1.77 GHz under the power cap).  With divisions for a block's
+// scale and position and 16 lanes a block it was 40.7 us, bound by issue.
 #pragma once
 
 #include "fp8_common.cuh"

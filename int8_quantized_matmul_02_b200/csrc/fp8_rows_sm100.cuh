@@ -64,12 +64,16 @@
 // At the end all but the first two join the shared tiles, a warp per row.
 //
 // Measured (calls back to back, weights from HBM): 1 x 12288 x 49152 95 us, 6.36
-// TB/s, which is what HBM gives; 8 x 4096 x 11008 12.0 us, of which 9 are the
-// stream of 86 blocks (56 to 60 GB/s each) and the rest the start and the first
-// boxes' latency; 16 x 256 x 384 3.8 us, all start; 100 x 11008 x 4096 18.5 us
-// and 333 x 4112 x 5136 20.6 us with the quantiser before, bound by shared
-// memory (a unit of 128 rows writes and reads 32 KB each, 512 cycles at 128
-// bytes a cycle, and takes ~670).  The gate/up kernel streams at 6.2 to 7 TB/s.
+// TB/s, which is what HBM gives (98 us in runs of seconds, at 1.73 GHz under the
+// power cap); 8 x 4096 x 11008 12.2 us, of which 9 are the stream of 86 blocks
+// (56 to 60 GB/s each) and the rest the start and the first boxes' latency; 16 x
+// 256 x 384 3.8 us on the GPU, all start; 100 x 11008 x 4096 19.5 us and 333 x
+// 4112 x 5136 21 us with the quantiser before.  In the first of these no unit of
+// the GPU is the bound (shared memory's banks 11 % of their peak for reads and
+// 11 % for writes, L2 20 %, HBM 27 %, tensor pipe 13 %, issue 43 %): a unit of
+// 128 rows takes ~670 cycles on its way round, 520 of them in the epilogue, and
+// the issuing thread waits 270 for a free accumulator.  The gate/up kernel
+// streams at 6.2 to 7 TB/s.
 #pragma once
 
 #include "fp8_common.cuh"
