@@ -420,7 +420,7 @@ def _on(device: torch.device, stream, *used):
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     for t in used:
-        if t is not None:
+        if t is not None and t.device == device:  # (others are refused by the checks that follow)
             t.record_stream(stream)
     return torch.cuda.stream(stream)
 

@@ -99,3 +99,36 @@ def test_everything_that_a_call_takes_is_recorded_on_its_stream(cuda_ok, monkeyp
         side.synchronize()
         torch.cuda.synchronize()
         assert not seen
+
+
+def test_tensors_that_a_call_refuses_are_refused_with_a_stream_too(cuda_ok):
+    g = torch.Generator(device="cuda").manual_seed(7)
+    side = torch.cuda.Stream()
+    X = torch.randn(24, 512, device="cuda", generator=g).half()
+    w, m = i8.weight_fp8(_codes(256, 512, g=g), torch.ones(2, 4, device="cuda")), _moe_weight(4, 512, 256, g)
+    for call in (lambda **kw: i8.forward_fp8(X, w, out=torch.empty(24, 256).half(), **kw),
+                 lambda **kw: i8.forward_fp8(X.cpu(), w, **kw),
+                 lambda **kw: i8.forward_moe_fp8(X, m, 2, out=torch.empty(24, 512).half(), **kw),
+                 lambda **kw: i8.quantize_fp8(X, codes=torch.empty(24, 512).to(torch.float8_e4m3fn), **kw),
+                 lambda **kw: i8.quantize_fp8(X, scales=torch.empty(24, 4), **kw)):
+        for kw in ({}, {"stream": side}):
+            with pytest.raises(ValueError):
+                call(**kw)
+
+
+@pytest.mark.parametrize("make", [_quantize, _product, _layer])
+def test_a_call_with_its_stream_named_in_a_capture(cuda_ok, make):
+    """stream= is the capturing stream; what was captured runs after the caller's
+    other tensors have come and gone."""
+    call = make(torch.Generator(device="cuda").manual_seed(8))
+    want = call(None).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = call(side)
+    torch.full((1 << 22,), 0x11, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        assert torch.equal(got, want)
