@@ -24,6 +24,9 @@ mixture-of-experts layer of them for a few tokens:
 These e4m3 calls take stream=s as a ``with torch.cuda.stream(s)`` around them
 does: s has to wait for whatever wrote the inputs, and what a call allocates
 belongs to s.  The memory of what a call is given is kept until s is done.
+The int8, 4-bit and codec calls launch on s too, but allocate on the current
+stream: with stream=s give them their outputs and workspace, and keep every
+tensor until s is done.
 """
 from __future__ import annotations
 
