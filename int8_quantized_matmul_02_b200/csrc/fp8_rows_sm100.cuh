@@ -70,10 +70,10 @@
 // 256 x 384 3.8 us on the GPU, all start; 100 x 11008 x 4096 19.5 us and 333 x
 // 4112 x 5136 21 us with the quantiser before.  In the first of these no unit of
 // the GPU is the bound (shared memory's banks 11 % of their peak for reads and
-// 11 % for writes, L2 20 %, HBM 27 %, tensor pipe 13 %, issue 43 %): a unit of
-// 128 rows takes ~670 cycles on its way round, 520 of them in the epilogue, and
-// the issuing thread waits 270 for a free accumulator.  The gate/up kernel
-// streams at 6.2 to 7 TB/s.
+// 11 % for writes, L2 20 %, HBM 27 %, tensor pipe 13 %, issue 43 %); in the
+// second a unit of 128 rows takes ~670 cycles on its way round, 520 of them in
+// the epilogue, and the issuing thread waits 270 for a free accumulator.  The
+// gate/up kernel streams at 6.2 to 7 TB/s.
 #pragma once
 
 #include "fp8_common.cuh"
