@@ -411,7 +411,7 @@ size_t int8mm_fp8_workspace_bytes(int M, int K, int N);
 /* Y (device, M x N) = X W, any M >= 1:
  *   Y[m,n] = 16-bit( sum_b xs[m,b] * ws[n/128,b] * sum_{k in block b} xq[m,k] wq[n,k] ),
  * with X's codes and scales formed by the call; the sums of a block are the
- * tensor cores' fp32 sums, the sum over blocks is fp32.  The result does not
+ * tensor cores' fp32 sums, xs * ws and the sum over blocks are fp32.  The result does not
  * depend on what else runs.  X and Y must not overlap.
  * opts may be NULL.  path: INT8MM_PATH_AUTO, _GEMM (tiled, SM pairs) or
  * _DECODE (weight-streaming, M <= 1024); acc_out must be NULL; events, wait
